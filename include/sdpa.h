@@ -388,6 +388,50 @@ sdpa_status_t sdpa_bwd_phases_varlen_ex(
     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Capped scores: the windowed calls with the score of every visible pair
+ * replaced by
+ *     S'' = softcap * tanh(S' / softcap),   S' = scale * Q K^T
+ * (masks apply afterwards), and in the backward dS' = dS'' (1 - (S''/softcap)^2).
+ *   softcap  in (0, 4096], with scale / softcap finite: SDPA_ERR_INVALID_ARG
+ *            otherwise. S'' is formed to softcap * 2^-21.
+ * The windows, the alignment, keep_bits, dropout, grouped heads, packed
+ * sequences, workspaces and phases are those of the sdpa_*_ex calls; there is
+ * no bias and no ALiBi. One call does the whole backward with SDPA_BWD_ALL.
+ */
+sdpa_status_t sdpa_fwd_capped(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t s_kv,
+                              int64_t d_qk, int64_t d_v, float scale, float softcap,
+                              int64_t window_left, int64_t window_right, int bottom_right,
+                              const uint32_t* keep_bits, uint32_t* keep_bits_out, float dropout_p,
+                              uint64_t seed, uint64_t offset, sdpa_dtype_t dtype, const void* q,
+                              const void* k, const void* v, void* o, float* lse, void* stream);
+sdpa_status_t sdpa_bwd_phases_capped(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s_q,
+                                     int64_t s_kv, int64_t d_qk, int64_t d_v, float scale,
+                                     float softcap, int64_t window_left, int64_t window_right,
+                                     int bottom_right, const uint32_t* keep_bits, float dropout_p,
+                                     uint64_t seed, uint64_t offset, sdpa_dtype_t dtype,
+                                     const void* q, const void* k, const void* v, const void* o,
+                                     const void* dout, const float* lse, void* dq, void* dk,
+                                     void* dv, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+sdpa_status_t sdpa_fwd_varlen_capped(int64_t b, int64_t h, int64_t h_kv, int64_t total_q,
+                                     int64_t total_k, int64_t max_seqlen_q, int64_t max_seqlen_k,
+                                     int64_t d_qk, int64_t d_v, float scale, float softcap,
+                                     int64_t window_left, int64_t window_right, int bottom_right,
+                                     const uint32_t* keep_bits, uint32_t* keep_bits_out,
+                                     float dropout_p, uint64_t seed, uint64_t offset,
+                                     sdpa_dtype_t dtype, const int32_t* seqstart_q,
+                                     const int32_t* seqstart_k, const void* q, const void* k,
+                                     const void* v, void* o, float* lse, void* stream);
+sdpa_status_t sdpa_bwd_phases_varlen_capped(
+    int phases, int64_t b, int64_t h, int64_t h_kv, int64_t total_q, int64_t total_k,
+    int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t d_qk, int64_t d_v, float scale,
+    float softcap, int64_t window_left, int64_t window_right, int bottom_right,
+    const uint32_t* keep_bits, float dropout_p, uint64_t seed, uint64_t offset, sdpa_dtype_t dtype,
+    const int32_t* seqstart_q, const int32_t* seqstart_k, const void* q, const void* k,
+    const void* v, const void* o, const void* dout, const float* lse, void* dq, void* dk, void* dv,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The backward pass for callers that cannot allocate device memory when they
  * run it (a host framework that owns all GPU memory through its own pool, or
  * a latency-critical loop that cannot afford cudaMalloc's implicit

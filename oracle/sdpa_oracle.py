@@ -83,6 +83,9 @@ class Problem:
     drop_frame: tuple | None = None
     # ALiBi slopes, [B][H] (nested sequences) or None
     alibi_slopes: tuple | None = None
+    # Scaled scores s become softcap * tanh(s / softcap) before the mask (no
+    # bias, no ALiBi); 0: not capped
+    softcap: float = 0.0
 
     def alibi_offset(self) -> int:
         """Diagonal of the ALiBi distance: top-left under a top-left mask."""
@@ -125,6 +128,9 @@ def scores(prob: Problem, q_h: np.ndarray, k_h: np.ndarray, bias_h, rows: np.nda
     CK tile fmha_bwd_kernel.hpp header: S = Q K^T, S' = S * Scale, S'' = S' + Bias.
     """
     s = prob.scale * (q_h[rows] @ k_h[cols].T)
+    if prob.softcap:
+        assert bias_h is None and slope == 0.0
+        s = prob.softcap * np.tanh(s / prob.softcap)
     if bias_h is not None:
         s = s + bias_h[np.ix_(rows, cols)]
     if slope != 0.0:  # ALiBi (module text)
@@ -213,13 +219,17 @@ def backward_head(prob: Problem, b: int, h: int, q, k, v, do, bias=None, rows=No
     bias_h = None if bias is None else _f64(bias[0, h])
 
     def grads_of_rows(rr, want_dq):
-        p, _ = softmax_rows(scores(prob, q_h, k_h, bias_h, rr, all_cols, alibi_slope(prob, b, h)))
+        s = scores(prob, q_h, k_h, bias_h, rr, all_cols, alibi_slope(prob, b, h))
+        p, _ = softmax_rows(s)
         z = dropout_scale(prob, b, h, rr, all_cols)
         pz = p * z
         o = pz @ v_h
         d = (do_h[rr] * o).sum(axis=1)
         dp = do_h[rr] @ v_h.T
         ds = p * (dp * z - d[:, None])
+        if prob.softcap:  # dS' = dS'' (1 - tanh^2); a masked score's P is 0
+            t = np.where(np.isfinite(s), s, 0.0) / prob.softcap
+            ds = ds * (1.0 - t * t)
         dq = prob.scale * (ds @ k_h) if want_dq else None
         return pz, ds, dq
 

@@ -57,6 +57,7 @@ class Packed:
     window: tuple | None = None  # as in sdpa_oracle.Problem, per sequence
     bottom_right: bool = False
     alibi_slopes: tuple | None = None  # [B][H], sequence i taking row i
+    softcap: float = 0.0  # as in sdpa_oracle.Problem
 
     @property
     def B(self) -> int:
@@ -81,7 +82,8 @@ class Packed:
         return so.Problem(1, self.H, lq, lk, self.D_qk, self.D_v, self.scale, self.is_causal,
                           self.dropout_p, self.seed, self.offset, self.H_kv, self.window,
                           self.bottom_right, drop_frame=(self.B, mq, mk, i),
-                          alibi_slopes=None if self.alibi_slopes is None else (self.alibi_slopes[i],))
+                          alibi_slopes=None if self.alibi_slopes is None else (self.alibi_slopes[i],),
+                          softcap=self.softcap)
 
 
 def _rows(x, a: int, b: int):

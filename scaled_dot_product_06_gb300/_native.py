@@ -74,6 +74,18 @@ SIGNATURES = {
     "sdpa_bwd_phases_varlen_ex": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _i64, _i64, _int, _ptr,
                                              _i64, _ptr, _f32, _u64, _u64, _int, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr,
                                              _ptr, _ptr, _sz, _ptr]),
+    "sdpa_fwd_capped": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _f32, _i64, _i64, _int, _ptr,
+                               _ptr, _f32, _u64, _u64, _int, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr]),
+    "sdpa_bwd_phases_capped": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _f32, _i64, _i64,
+                                      _int, _ptr, _f32, _u64, _u64, _int, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr,
+                                      _ptr, _ptr, _ptr, _ptr, _sz, _ptr]),
+    "sdpa_fwd_varlen_capped": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _f32, _i64,
+                                      _i64, _int, _ptr, _ptr, _f32, _u64, _u64, _int, _ptr, _ptr, _ptr, _ptr,
+                                      _ptr, _ptr, _ptr, _ptr]),
+    "sdpa_bwd_phases_varlen_capped": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _f32,
+                                             _f32, _i64, _i64, _int, _ptr, _f32, _u64, _u64, _int, _ptr, _ptr,
+                                             _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _sz,
+                                             _ptr]),
     "sdpa_bwd_noalloc": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _f32, _int, _f32, _u64, _u64,
                                 _int, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr,
                                 _ptr, _ptr]),

@@ -76,6 +76,18 @@ def _window(is_causal, window, bottom_right, alibi_slopes, n_batch, h, dropout_m
     return int(left), int(right), int(bool(bottom_right)), _ptr(alibi_slopes), stride, _ptr(dropout_mask)
 
 
+def _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, n_batch, h, dropout_mask):
+    """(softcap, left, right, bottom_right, keep-bits pointer) for the *_capped
+    entry points, or None for uncapped scores (softcap None or 0)."""
+    if softcap is None or softcap == 0:
+        return None
+    if bias is not None or alibi_slopes is not None:
+        raise ValueError("softcap takes no bias and no alibi_slopes")
+    left, right, br, _, _, keep = _window(is_causal, window, bottom_right, None, n_batch, h,
+                                          dropout_mask, force=True)
+    return float(softcap), left, right, br, keep
+
+
 def _mask_out(t, words):
     """A forward's keep-bit record buffer: contiguous int32 CUDA words."""
     if t is None:
@@ -88,7 +100,7 @@ def _mask_out(t, words):
 
 def sdpa_fwd(q, k, v, *, scale=None, is_causal=False, dropout_p=0.0, seed=0, offset=0,
              bias=None, out=None, lse=None, stream=None, window=None, bottom_right=False,
-             alibi_slopes=None, dropout_mask=None, dropout_mask_out=None):
+             alibi_slopes=None, dropout_mask=None, dropout_mask_out=None, softcap=None):
     """Forward pass. Returns (o [b,h,s_q,d_v], lse fp32 [b,h,s_q]).
 
     k and v may have fewer heads than q (grouped-query attention): h_kv =
@@ -100,7 +112,9 @@ def sdpa_fwd(q, k, v, *, scale=None, is_causal=False, dropout_p=0.0, seed=0, off
     scaled scores, off_a = 0 under a top-left window, else s_kv - s_q.
     dropout_mask_out (int32 CUDA, ceil(b*h*s_q*s_kv/32) words): the forward
     records the dropout keep bits it draws there, for sdpa_bwd's
-    dropout_mask (needs s_kv % 32 == 0)."""
+    dropout_mask (needs s_kv % 32 == 0).
+    softcap (in (0, 4096]; None or 0: none) replaces each scaled score s by
+    softcap * tanh(s / softcap) before the mask; not with a bias or ALiBi."""
     b, h, s_q, d_qk = q.shape
     h_kv, s_kv, d_v = k.shape[1], k.shape[2], v.shape[3]
     dt = q.dtype
@@ -118,6 +132,15 @@ def sdpa_fwd(q, k, v, *, scale=None, is_causal=False, dropout_p=0.0, seed=0, off
         lse = torch.empty((b, h, s_q), dtype=torch.float32, device=q.device)
     _check_io("out", out, (b, h, s_q, d_v), dt)
     _check_io("lse", lse, (b, h, s_q), torch.float32)
+    cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask)
+    if cap is not None:
+        rec = _mask_out(dropout_mask_out, (b * h * s_q * s_kv + 31) // 32)
+        st = _native.lib().sdpa_fwd_capped(b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *cap, rec,
+                                           float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt],
+                                           _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                           _stream_ptr(stream, q))
+        _native.check(st, "sdpa_fwd_capped")
+        return out, lse
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask,
                 force=dropout_mask_out is not None)
     if w is None:
@@ -153,7 +176,7 @@ def _workspace_size(b, h, h_kv, s_q, s_kv, d_qk, d_v, deterministic) -> int:
 def sdpa_bwd(q, k, v, o, dout, lse, *, scale=None, is_causal=False, dropout_p=0.0, seed=0,
              offset=0, bias=None, workspace=None, dq=None, dk=None, dv=None, dbias=None,
              stream=None, window=None, bottom_right=False, alibi_slopes=None,
-             dropout_mask=None, deterministic=False):
+             dropout_mask=None, deterministic=False, softcap=None):
     """Backward pass. Returns (dq, dk, dv, dbias or None); dk and dv have k's
     and v's shapes (with grouped K/V heads, sums over each group).
     deterministic=True runs the deterministic backward (dQ from the
@@ -164,13 +187,13 @@ def sdpa_bwd(q, k, v, o, dout, lse, *, scale=None, is_causal=False, dropout_p=0.
                            bias=bias, workspace=workspace, dq=dq, dk=dk, dv=dv, dbias=dbias,
                            stream=stream, window=window, bottom_right=bottom_right,
                            alibi_slopes=alibi_slopes, dropout_mask=dropout_mask,
-                           deterministic=deterministic)
+                           deterministic=deterministic, softcap=softcap)
 
 
 def sdpa_bwd_phases(phases, q, k, v, o, dout, lse, *, scale=None, is_causal=False, dropout_p=0.0,
                     seed=0, offset=0, bias=None, workspace=None, dq=None, dk=None, dv=None,
                     dbias=None, stream=None, window=None, bottom_right=False, alibi_slopes=None,
-                    dropout_mask=None, deterministic=False):
+                    dropout_mask=None, deterministic=False, softcap=None):
     """The backward phases selected by ``phases`` (SDPA_BWD_* bit mask; the
     SDPA_BWD_DETERMINISTIC bit, or deterministic=True, selects the
     deterministic backward)."""
@@ -197,6 +220,14 @@ def sdpa_bwd_phases(phases, q, k, v, o, dout, lse, *, scale=None, is_causal=Fals
     need = sdpa_bwd_workspace_size(b, h, s_q, s_kv, d_qk, d_v, h_kv, deterministic)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask)
+    if cap is not None:
+        st = _native.lib().sdpa_bwd_phases_capped(
+            int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *cap, float(dropout_p), int(seed),
+            int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
+            _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _stream_ptr(stream, q))
+        _native.check(st, "sdpa_bwd_phases_capped")
+        return dq, dk, dv, None
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask)
     if w is None:
         st = _native.lib().sdpa_bwd_phases_gqa(
@@ -226,7 +257,7 @@ def _check_seqstart(name: str, t: torch.Tensor) -> int:
 def sdpa_fwd_varlen(q, k, v, seqstart_q, seqstart_k, max_seqlen_q, max_seqlen_k, *, scale=None,
                     is_causal=False, dropout_p=0.0, seed=0, offset=0, out=None, lse=None,
                     stream=None, window=None, bottom_right=False, alibi_slopes=None,
-                    dropout_mask=None, dropout_mask_out=None):
+                    dropout_mask=None, dropout_mask_out=None, softcap=None):
     """Forward pass over packed variable-length sequences. q [h, total_q, d_qk],
     k [h_kv, total_k, d_qk], v [h_kv, total_k, d_v]; seqstart_q / seqstart_k
     int32 CUDA tensors of b + 1 row offsets (sequence i owns query rows
@@ -250,6 +281,15 @@ def sdpa_fwd_varlen(q, k, v, seqstart_q, seqstart_k, max_seqlen_q, max_seqlen_k,
         lse = torch.empty((h, total_q), dtype=torch.float32, device=q.device)
     _check_io("out", out, (h, total_q, d_v), dt)
     _check_io("lse", lse, (h, total_q), torch.float32)
+    cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask)
+    if cap is not None:
+        rec = _mask_out(dropout_mask_out, (b * h * int(max_seqlen_q) * int(max_seqlen_k) + 31) // 32)
+        st = _native.lib().sdpa_fwd_varlen_capped(
+            b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v, scale, *cap,
+            rec, float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q),
+            _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _stream_ptr(stream, q))
+        _native.check(st, "sdpa_fwd_varlen_capped")
+        return out, lse
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask,
                 force=dropout_mask_out is not None)
     if w is None:
@@ -284,7 +324,7 @@ def sdpa_bwd_varlen_workspace_size(b, h, total_q, d_qk=None, deterministic=False
 def sdpa_bwd_varlen(q, k, v, o, dout, lse, seqstart_q, seqstart_k, max_seqlen_q, max_seqlen_k, *,
                     scale=None, is_causal=False, dropout_p=0.0, seed=0, offset=0, workspace=None,
                     dq=None, dk=None, dv=None, stream=None, window=None, bottom_right=False,
-                    alibi_slopes=None, dropout_mask=None, deterministic=False):
+                    alibi_slopes=None, dropout_mask=None, deterministic=False, softcap=None):
     """Backward pass over packed sequences (layouts as sdpa_fwd_varlen).
     Returns (dq, dk, dv) shaped like q, k, v. deterministic=True runs the
     deterministic backward, as sdpa_bwd."""
@@ -294,14 +334,14 @@ def sdpa_bwd_varlen(q, k, v, o, dout, lse, seqstart_q, seqstart_k, max_seqlen_q,
                                   offset=offset, workspace=workspace, dq=dq, dk=dk, dv=dv,
                                   stream=stream, window=window, bottom_right=bottom_right,
                                   alibi_slopes=alibi_slopes, dropout_mask=dropout_mask,
-                                  deterministic=deterministic)
+                                  deterministic=deterministic, softcap=softcap)
 
 
 def sdpa_bwd_phases_varlen(phases, q, k, v, o, dout, lse, seqstart_q, seqstart_k, max_seqlen_q,
                            max_seqlen_k, *, scale=None, is_causal=False, dropout_p=0.0, seed=0,
                            offset=0, workspace=None, dq=None, dk=None, dv=None, stream=None,
                            window=None, bottom_right=False, alibi_slopes=None,
-                           dropout_mask=None, deterministic=False):
+                           dropout_mask=None, deterministic=False, softcap=None):
     """The packed-sequence backward phases selected by ``phases`` (the
     SDPA_BWD_DETERMINISTIC bit, or deterministic=True, selects the
     deterministic backward). A caller-given workspace smaller than the
@@ -328,6 +368,15 @@ def sdpa_bwd_phases_varlen(phases, q, k, v, o, dout, lse, seqstart_q, seqstart_k
     need = sdpa_bwd_varlen_workspace_size(b, h, total_q, d_qk, deterministic)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask)
+    if cap is not None:
+        st = _native.lib().sdpa_bwd_phases_varlen_capped(
+            int(phases), b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v,
+            scale, *cap, float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q),
+            _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
+            _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _stream_ptr(stream, q))
+        _native.check(st, "sdpa_bwd_phases_varlen_capped")
+        return dq, dk, dv
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask)
     if w is None:
         st = _native.lib().sdpa_bwd_phases_varlen(

@@ -253,6 +253,8 @@ struct Mask {
   int64_t alibi_stride = 0;
   const uint32_t* keep_bits = nullptr;  // dropout keep bits drawn beforehand (device)
   uint32_t* keep_out = nullptr;         // forward: record of the keep bits it draws (device)
+  bool capped = false;                  // scores softcap * tanh(S * scale / softcap) (no bias or ALiBi)
+  float softcap = 0.f;
 };
 Mask causal_mask(int is_causal) { return Mask{-1, is_causal ? 0 : -1, 0}; }
 
@@ -285,6 +287,20 @@ sdpa_status_t check_alibi(const Mask& mk, int64_t b, int64_t h) {
   if (mk.alibi_stride < 0 || (mk.alibi_stride > 0 && mk.alibi_stride < h) ||
       (b - 1) * mk.alibi_stride + h > (int64_t{1} << 30))
     return fail(SDPA_ERR_INVALID_ARG, "alibi_stride");
+  return SDPA_OK;
+}
+
+// The cap of a capped call: in (0, kMaxSoftcap], with a slope scale / softcap
+// whose product with 2 log2(e) is finite. The kernels form the capped score as
+// softcap - 2 softcap r with r off by 2^-21 relative, so above 4096 the score
+// would be off by more than 2^-9, half a bf16 rounding of P.
+constexpr float kMaxSoftcap = 4096.f;
+sdpa_status_t check_softcap(const Mask& mk, float scale) {
+  if (!mk.capped) return SDPA_OK;
+  if (!(mk.softcap > 0.f && mk.softcap <= kMaxSoftcap))
+    return fail(SDPA_ERR_INVALID_ARG, "softcap must lie in (0, 4096]");
+  if (!std::isfinite(2.f * kLog2e * scale / mk.softcap))
+    return fail(SDPA_ERR_INVALID_ARG, "scale / softcap must be finite");
   return SDPA_OK;
 }
 
@@ -428,6 +444,7 @@ sdpa_status_t fwd_impl(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t 
   if (!kv_heads_ok(h, h_kv)) return fail(SDPA_ERR_INVALID_ARG, "h_kv must divide h");
   if (sdpa_status_t s = check_packing(pk, b, bias, &empty)) return s;
   if (sdpa_status_t s = check_alibi(mask, b, h)) return s;
+  if (sdpa_status_t s = check_softcap(mask, scale)) return s;
   if (dropout_p > 0.0f && mask.keep_out != nullptr) {  // a record of the keep bits drawn
     if (mask.keep_bits != nullptr)
       return fail(SDPA_ERR_INVALID_ARG, "keep_bits and keep_bits_out together");
@@ -454,6 +471,11 @@ sdpa_status_t fwd_impl(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t 
   p.S_q = static_cast<int>(s_q);
   p.S_kv = static_cast<int>(s_kv);
   p.scale_log2 = scale * kLog2e;
+  if (mask.capped) {
+    p.softcap = mask.softcap;
+    p.cap_in = 2.f * kLog2e * scale / mask.softcap;
+    p.scale_log2 = -2.f * kLog2e * mask.softcap;
+  }
   set_window(mask, s_q, s_kv, &p);
   if (dropout_p > 0.0f && mask.keep_bits != nullptr) {  // bits drawn beforehand, [b, h, s_q, s_kv] frame
     p.keep_bits = mask.keep_bits;
@@ -492,8 +514,10 @@ sdpa_status_t fwd_impl(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t 
     p.keep_out = nullptr;
   }
   if (sdpa_status_t s = error_word_ptr(&p.err)) return s;
-  const cudaError_t e = bf16 ? launch_fwd_bf16(static_cast<int>(d_qk), static_cast<int>(d_v), mq, mk, mv, p, st)
-                             : launch_fwd_fp16(static_cast<int>(d_qk), static_cast<int>(d_v), mq, mk, mv, p, st);
+  const cudaError_t e =
+      mask.capped ? launch_fwd_cap(bf16, static_cast<int>(d_qk), static_cast<int>(d_v), mq, mk, mv, p, st)
+      : bf16      ? launch_fwd_bf16(static_cast<int>(d_qk), static_cast<int>(d_v), mq, mk, mv, p, st)
+                  : launch_fwd_fp16(static_cast<int>(d_qk), static_cast<int>(d_v), mq, mk, mv, p, st);
   return cuda_status(e, "forward kernel launch");
 }
 
@@ -513,6 +537,7 @@ sdpa_status_t bwd_impl(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s
   if (!kv_heads_ok(h, h_kv)) return fail(SDPA_ERR_INVALID_ARG, "h_kv must divide h");
   if (sdpa_status_t s = check_packing(pk, b, bias, &empty)) return s;
   if (sdpa_status_t s = check_alibi(mask, b, h)) return s;
+  if (sdpa_status_t s = check_softcap(mask, scale)) return s;
   if (empty) return SDPA_OK;
   if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv) return SDPA_ERR_INVALID_ARG;
   if ((bias == nullptr) != (dbias == nullptr)) return SDPA_ERR_INVALID_ARG;
@@ -549,6 +574,11 @@ sdpa_status_t bwd_impl(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s
   p.S_kv = static_cast<int>(s_kv);
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
+  if (mask.capped) {
+    p.softcap = mask.softcap;
+    p.cap_in = 2.f * kLog2e * scale / mask.softcap;
+    p.cap_out = -2.f * kLog2e * mask.softcap;
+  }
   set_window(mask, s_q, s_kv, &p);
   if (dropout_p > 0.0f && mask.keep_bits != nullptr) {  // bits drawn beforehand, [b, h, s_q, s_kv] frame
     p.keep_bits = mask.keep_bits;
@@ -581,7 +611,7 @@ sdpa_status_t bwd_impl(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s
   // registers).
   bool dq_direct = false;
   if (fused && pk.seqstart_q == nullptr && s_kv <= 128 && kv_split <= 1) {
-    const bool win = p.win_general || p.alibi != nullptr;  // the kernel instance's band
+    const bool win = p.win_general || p.alibi != nullptr || mask.capped;  // the kernel instance's band
     const sdpa::Band bd = win ? sdpa::band_of(p.win_left, p.win_right, p.win_br, p.S_q, p.S_kv)
                               : sdpa::plain_band(p.win_right);
     const sdpa::TileRange r = sdpa::query_tiles_of_keys(win, bd, p.win_right, 0, 128, 128, p.S_q, p.S_kv);
@@ -610,7 +640,7 @@ sdpa_status_t bwd_impl(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s
     const int64_t dbias_elems = (bias && fused) ? h * s_q * s_kv : 0;
     e = launch_bwd_pre(bf16, o, dout, lse, stats, dbias, rw.zq, static_cast<int>(s_q), p.S_pad, p.rows_q,
                        pk.seqstart_q, static_cast<int>(b), dvi, dbias_elems, p.dkdv_count, n_counters,
-                       p.dq_acc, dq_acc_elems, st);
+                       p.dq_acc, dq_acc_elems, mask.capped ? kLog2e * mask.softcap : 0.f, st);
     if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "backward preprocess launch", e);
   }
   // Both main kernels requested: dK/dV on the side stream, forked after the
@@ -647,12 +677,13 @@ sdpa_status_t bwd_impl(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s
       return ms;
     }
     if (fused) {
-      e = bf16 ? launch_bwd_fused_bf16(di, dvi, mq, mk, mv, mdo, mdk, mdv, p, st_dkdv)
+      e = mask.capped ? launch_bwd_fused_cap(bf16, di, dvi, mq, mk, mv, mdo, mdk, mdv, p, st_dkdv)
+          : bf16 ? launch_bwd_fused_bf16(di, dvi, mq, mk, mv, mdo, mdk, mdv, p, st_dkdv)
                : launch_bwd_fused_fp16(di, dvi, mq, mk, mv, mdo, mdk, mdv, p, st_dkdv);
     } else {
       if (bias != nullptr) {  // dBias = 0 ahead of the kernel's fp32 reductions into it
         e = launch_bwd_pre(bf16, o, dout, lse, stats, dbias, 0, static_cast<int>(s_q), p.S_pad, p.rows_q,
-                           nullptr, static_cast<int>(b), dvi, h * s_q * s_kv, nullptr, 0, nullptr, 0, st_dkdv);
+                           nullptr, static_cast<int>(b), dvi, h * s_q * s_kv, nullptr, 0, nullptr, 0, 0.f, st_dkdv);
         if (e != cudaSuccess) {
           join();
           return fail(SDPA_ERR_CUDA, "backward dBias zero pass launch", e);
@@ -666,7 +697,11 @@ sdpa_status_t bwd_impl(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s
       if (bias != nullptr && d_qk != 128 && s_kv % 4 == 0 &&
           encode_bias_map(&mb, bias, h, s_q, s_kv, 128, q_rows, false) == SDPA_OK)
         p.bias_tma = 1;
-      e = bf16 ? launch_bwd_dkdv_bf16(di, dvi, mq, mk, mv, mdo, mb, mdk, mdv, p, st_dkdv)
+      if (mask.capped)
+        e = bf16 ? launch_bwd_dkdv_cap_bf16(di, dvi, mq, mk, mv, mdo, mdk, mdv, p, st_dkdv)
+                 : launch_bwd_dkdv_cap_fp16(di, dvi, mq, mk, mv, mdo, mdk, mdv, p, st_dkdv);
+      else
+        e = bf16 ? launch_bwd_dkdv_bf16(di, dvi, mq, mk, mv, mdo, mb, mdk, mdv, p, st_dkdv)
                : launch_bwd_dkdv_fp16(di, dvi, mq, mk, mv, mdo, mb, mdk, mdv, p, st_dkdv);
     }
     if (e != cudaSuccess) {
@@ -699,7 +734,8 @@ sdpa_status_t bwd_impl(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s
     if (bias != nullptr && d_qk != 128 && s_kv % 4 == 0 &&
         encode_bias_map(&mb, bias, h, s_q, s_kv, 32, 128, true) == SDPA_OK)
       p.bias_tma = 1;
-    e = bf16 ? launch_bwd_dq_bf16(di, dvi, mq, mk, mv, mdo, mb, mdq, p, st)
+    e = mask.capped ? launch_bwd_dq_cap(bf16, di, dvi, mq, mk, mv, mdo, mdq, p, st)
+        : bf16 ? launch_bwd_dq_bf16(di, dvi, mq, mk, mv, mdo, mb, mdq, p, st)
              : launch_bwd_dq_fp16(di, dvi, mq, mk, mv, mdo, mb, mdq, p, st);
     if (e != cudaSuccess) {
       join();
@@ -992,6 +1028,72 @@ sdpa_status_t sdpa_bwd_varlen_ex(int64_t b, int64_t h, int64_t h_kv, int64_t tot
                                        bottom_right, alibi_slopes, alibi_stride, keep_bits, dropout_p, seed,
                                        offset, dtype, seqstart_q, seqstart_k, q, k, v, o, dout, lse,
                                        dq, dk, dv, workspace, workspace_bytes, stream);
+}
+
+// Capped scores (batch and packed forms).
+static Mask capped_mask(float softcap, int64_t window_left, int64_t window_right, int bottom_right,
+                        const uint32_t* keep_bits, uint32_t* keep_bits_out) {
+  return Mask{window_left, window_right, bottom_right, nullptr, 0, keep_bits, keep_bits_out, true, softcap};
+}
+
+sdpa_status_t sdpa_fwd_capped(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t s_kv, int64_t d_qk,
+                              int64_t d_v, float scale, float softcap, int64_t window_left,
+                              int64_t window_right, int bottom_right, const uint32_t* keep_bits,
+                              uint32_t* keep_bits_out, float dropout_p, uint64_t seed, uint64_t offset,
+                              sdpa_dtype_t dtype, const void* q, const void* k, const void* v, void* o,
+                              float* lse, void* stream) {
+  return fwd_impl(b, h, h_kv, s_q, s_kv, d_qk, d_v, scale,
+                  capped_mask(softcap, window_left, window_right, bottom_right, keep_bits, keep_bits_out),
+                  dropout_p, seed, offset, dtype, q, k, v, nullptr, o, lse, stream, Packing{});
+}
+
+sdpa_status_t sdpa_bwd_phases_capped(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s_q,
+                                     int64_t s_kv, int64_t d_qk, int64_t d_v, float scale, float softcap,
+                                     int64_t window_left, int64_t window_right, int bottom_right,
+                                     const uint32_t* keep_bits, float dropout_p, uint64_t seed,
+                                     uint64_t offset, sdpa_dtype_t dtype, const void* q, const void* k,
+                                     const void* v, const void* o, const void* dout, const float* lse,
+                                     void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  return bwd_impl(phases, b, h, h_kv, s_q, s_kv, d_qk, d_v, scale,
+                  capped_mask(softcap, window_left, window_right, bottom_right, keep_bits, nullptr),
+                  dropout_p, seed, offset, dtype, q, k, v, nullptr, o, dout, lse, dq, dk, dv, nullptr,
+                  workspace, workspace_bytes, stream, Packing{});
+}
+
+sdpa_status_t sdpa_fwd_varlen_capped(int64_t b, int64_t h, int64_t h_kv, int64_t total_q, int64_t total_k,
+                                     int64_t max_seqlen_q, int64_t max_seqlen_k, int64_t d_qk, int64_t d_v,
+                                     float scale, float softcap, int64_t window_left, int64_t window_right,
+                                     int bottom_right, const uint32_t* keep_bits, uint32_t* keep_bits_out,
+                                     float dropout_p, uint64_t seed, uint64_t offset, sdpa_dtype_t dtype,
+                                     const int32_t* seqstart_q, const int32_t* seqstart_k, const void* q,
+                                     const void* k, const void* v, void* o, float* lse, void* stream) {
+  const Packing pk{seqstart_q, seqstart_k, total_q, total_k};
+  if (seqstart_q == nullptr || seqstart_k == nullptr) {
+    if (b == 0 || h == 0 || total_q == 0 || total_k == 0) return SDPA_OK;
+    return fail(SDPA_ERR_INVALID_ARG, "seqstart_q and seqstart_k are required");
+  }
+  return fwd_impl(b, h, h_kv, max_seqlen_q, max_seqlen_k, d_qk, d_v, scale,
+                  capped_mask(softcap, window_left, window_right, bottom_right, keep_bits, keep_bits_out),
+                  dropout_p, seed, offset, dtype, q, k, v, nullptr, o, lse, stream, pk);
+}
+
+sdpa_status_t sdpa_bwd_phases_varlen_capped(
+    int phases, int64_t b, int64_t h, int64_t h_kv, int64_t total_q, int64_t total_k, int64_t max_seqlen_q,
+    int64_t max_seqlen_k, int64_t d_qk, int64_t d_v, float scale, float softcap, int64_t window_left,
+    int64_t window_right, int bottom_right, const uint32_t* keep_bits, float dropout_p, uint64_t seed,
+    uint64_t offset, sdpa_dtype_t dtype, const int32_t* seqstart_q, const int32_t* seqstart_k, const void* q,
+    const void* k, const void* v, const void* o, const void* dout, const float* lse, void* dq, void* dk,
+    void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  const Packing pk{seqstart_q, seqstart_k, total_q, total_k};
+  if (seqstart_q == nullptr || seqstart_k == nullptr) {
+    if (b == 0 || h == 0 || total_q == 0 || total_k == 0) return SDPA_OK;
+    return fail(SDPA_ERR_INVALID_ARG, "seqstart_q and seqstart_k are required");
+  }
+  return bwd_impl(phases, b, h, h_kv, max_seqlen_q, max_seqlen_k, d_qk, d_v, scale,
+                  capped_mask(softcap, window_left, window_right, bottom_right, keep_bits, nullptr),
+                  dropout_p, seed, offset, dtype, q, k, v, nullptr, o, dout, lse, dq, dk, dv, nullptr,
+                  workspace, workspace_bytes, stream, pk);
 }
 
 sdpa_status_t sdpa_bwd_gqa(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t s_kv,

@@ -2,7 +2,8 @@
 //
 // * bwd_pre: D = rowsum(dO * O) in fp32 (CK tile fmha_bwd_kernel.hpp,
 //   FmhaBwdOGradDotOKernel; the D line of the header equations) next to
-//   -LSE * log2(e), in the tiled row-statistics layout of stat_index, and zeroing
+//   -LSE * log2(e) (plus lse_shift, softcap * log2(e) for capped scores), in the
+//   tiled row-statistics layout of stat_index, and zeroing
 //   of dBias, which the key/value-stationary kernel accumulates into (oneDNN
 //   sdpa micro.cpp, execute_backward: preprocess and fill of the f32
 //   intermediates), and of the fused backward's fp32 dQ accumulator.
@@ -43,7 +44,7 @@ __global__ void __launch_bounds__(kAuxThreads) bwd_pre_kernel(const uint4* __res
                                                               int n_seq, int d_v, int64_t dbias_elems,
                                                               int* __restrict__ counters, int n_counters,
                                                               float4* __restrict__ dq_acc,
-                                                              int64_t dq_acc_vec) {
+                                                              int64_t dq_acc_vec, float lse_shift) {
   const int group = d_v / 8;  // 8 or 16 threads per row (power of two)
   const int64_t tid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t nthreads = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kAuxThreads) bwd_pre_kernel(const uint4* __res
     if (prow < prow_count && sub == 0) {
       const float L = live ? lse[row] : SDPA_NEG_INF;
       const size_t si = stat_index(static_cast<size_t>(z), s_pad, r);
-      stats[si] = (L == SDPA_NEG_INF) ? SDPA_NEG_INF : -L * kLog2e;
+      stats[si] = (L == SDPA_NEG_INF) ? SDPA_NEG_INF : fmaf(-L, kLog2e, lse_shift);
       stats[si + 64] = -acc;
     }
   }
@@ -167,7 +168,7 @@ cudaError_t launch_bwd_pre(bool bf16, const void* o, const void* dout, const flo
                            float* dbias, int64_t z_count, int s_q, int s_pad, int rows,
                            const int* seqstart, int n_seq, int d_v, int64_t dbias_elems,
                            int* counters, int n_counters, float* dq_acc, int64_t dq_acc_elems,
-                           cudaStream_t st) {
+                           float lse_shift, cudaStream_t st) {
   const int group = d_v / 8;
   const int64_t work = z_count * s_pad * group;
   const int64_t zero_work = (dbias_elems + dq_acc_elems) / 4;
@@ -176,7 +177,7 @@ cudaError_t launch_bwd_pre(bool bf16, const void* o, const void* dout, const flo
   kern<<<grid, kAuxThreads, 0, st>>>(static_cast<const uint4*>(o), static_cast<const uint4*>(dout), lse, stats,
                                       reinterpret_cast<float4*>(dbias), z_count, s_q, s_pad, rows, seqstart,
                                       n_seq, d_v, dbias_elems, counters, n_counters,
-                                      reinterpret_cast<float4*>(dq_acc), dq_acc_elems / 4);
+                                      reinterpret_cast<float4*>(dq_acc), dq_acc_elems / 4, lse_shift);
   return cudaGetLastError();
 }
 

@@ -241,7 +241,7 @@ __device__ __noinline__ void split_epilogue(float* dkdv_part, int* dkdv_count, i
 // window or the bottom-right alignment) likewise: the plain kernel masks only
 // the top-left causal diagonal. SPLIT (kv_split > 1) likewise: its epilogue
 // keeps the key tile's indices and the partial-row code out of the others.
-template <int DQK, int DV, bool BF16, bool DROP, bool BIAS, bool WIN, bool SPLIT>
+template <int DQK, int DV, bool BF16, bool DROP, bool BIAS, bool WIN, bool SPLIT, bool CAP = false>
 __global__ void __launch_bounds__(DkdvCfg<DQK, DV>::THREADS, 1)
     sdpa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
@@ -577,6 +577,21 @@ __global__ void __launch_bounds__(DkdvCfg<DQK, DV>::THREADS, 1)
         // same barrier makes the statistics visible to this thread too
         if (!(ok = mbar_wait(bar(AB_QF + (i & 1)), (i >> 1) & 1, ec, kSiteBwdCompute))) break;
         tc_fence_after();
+        // CAP: P packed for dV (pwc) and pr = P (1 - tanh^2)
+        uint32_t pwc[16];
+        if constexpr (CAP) {
+          tmem_ld32f(tbase + C::T_S + lane_off + CW * hf, pr);
+          tmem_wait_ld();
+          tc_fence_before();
+          mbar_arrive(bar(AB_SFREE));  // S^T(i) is in registers
+          cap_probs<BF16>(pr, pwc, p.cap_in, p.cap_out, [&](int e4) { return lds128(nl2_s + 16u * e4); }, zf);
+          const Band wb = lds_band(band_slot);
+          if ((qc0 < k0 + C::BN - 1 - wb.hi) || (qc0 + CW - 1 > k0 - wb.lo) || (qc0 + CW > S_q) || !kv_ok) {
+            const int first = kv - wb.hi - qc0;  // visible local columns [first, lim)
+            const int lim = kv_ok ? min(CW, min(S_q - 1, kv - wb.lo) + 1 - qc0) : 0;
+            cap_mask(pr, pwc, [&](int c) { return c < first || c >= lim; });
+          }
+        } else {
 #pragma unroll
         for (int c = 0; c < CW / 32; ++c) {
           uint32_t a0[32];
@@ -634,6 +649,7 @@ __global__ void __launch_bounds__(DkdvCfg<DQK, DV>::THREADS, 1)
         }
 #pragma unroll
         for (int c = 0; c < CW; ++c) pr[c] = ex2(pr[c]);
+        }
         if (!(ok = mbar_wait(bar(AB_DP), i & 1, ec, kSiteBwdCompute))) break;
         tc_fence_after();
         // The thread's 32 dP^T columns are handled in halves of 16 so that at
@@ -679,7 +695,8 @@ __global__ void __launch_bounds__(DkdvCfg<DQK, DV>::THREADS, 1)
           tmem_ld16(tcol, lo);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pw[e] = pack2<BF16>(pr[2 * e] * zf(2 * e), pr[2 * e + 1] * zf(2 * e + 1));
+          for (int e = 0; e < 16; ++e)
+            pw[e] = CAP ? pwc[e] : pack2<BF16>(pr[2 * e] * zf(2 * e), pr[2 * e + 1] * zf(2 * e + 1));
           tmem_st16(tcol, pw);
           tmem_wait_st();
           tc_fence_before();
@@ -811,6 +828,18 @@ __global__ void __launch_bounds__(DkdvCfg<DQK, DV>::THREADS, 1)
   }
 }
 
+template <typename C, typename Kern>
+cudaError_t launch_dkdv_kernel(Kern kern, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                               const CUtensorMap& dout, const CUtensorMap& bias_map, const CUtensorMap& dk,
+                               const CUtensorMap& dv, const BwdParams& p, cudaStream_t st) {
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, 0);
+  if (e != cudaSuccess) return e;
+  const int n_kt = (p.S_kv + C::BN - 1) / C::BN;
+  const long long grid = static_cast<long long>(n_kt) * p.B * p.H_kv * p.kv_split;
+  kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, st>>>(q, k, v, dout, bias_map, dk, dv, p);
+  return cudaGetLastError();
+}
+
 template <int DQK, int DV, bool BF16>
 cudaError_t launch_bwd_dkdv_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                               const CUtensorMap& dout, const CUtensorMap& bias_map, const CUtensorMap& dk,
@@ -829,12 +858,22 @@ cudaError_t launch_bwd_dkdv_t(const CUtensorMap& q, const CUtensorMap& k, const 
                                     : pick(std::false_type{}, std::true_type{}))
                              : (win ? pick(std::true_type{}, std::false_type{})
                                     : pick(std::false_type{}, std::false_type{}));
-  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, 0);
-  if (e != cudaSuccess) return e;
-  const int n_kt = (p.S_kv + C::BN - 1) / C::BN;
-  const long long grid = static_cast<long long>(n_kt) * p.B * p.H_kv * p.kv_split;
-  kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, st>>>(q, k, v, dout, bias_map, dk, dv, p);
-  return cudaGetLastError();
+  return launch_dkdv_kernel<C>(kern, q, k, v, dout, bias_map, dk, dv, p, st);
+}
+
+// Capped scores (p.softcap > 0, no bias or ALiBi): the windowed kernels, which
+// also run the plain masks.
+template <int DQK, int DV, bool BF16>
+cudaError_t launch_bwd_dkdv_cap_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                  const CUtensorMap& dout, const CUtensorMap& dk, const CUtensorMap& dv,
+                                  const BwdParams& p, cudaStream_t st) {
+  auto pick = [&](auto split) {
+    constexpr bool SP = decltype(split)::value;
+    return p.dropout ? sdpa_bwd_dkdv_kernel<DQK, DV, BF16, true, false, true, SP, true>
+                     : sdpa_bwd_dkdv_kernel<DQK, DV, BF16, false, false, true, SP, true>;
+  };
+  auto kern = p.kv_split > 1 ? pick(std::true_type{}) : pick(std::false_type{});
+  return launch_dkdv_kernel<DkdvCfg<DQK, DV>>(kern, q, k, v, dout, CUtensorMap{}, dk, dv, p, st);
 }
 
 }  // namespace sdpa

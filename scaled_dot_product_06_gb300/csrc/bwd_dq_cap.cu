@@ -1,0 +1,18 @@
+// Capped-score dQ kernel instantiations.
+#include "bwd_dq_kernel.cuh"
+
+namespace sdpa {
+
+cudaError_t launch_bwd_dq_cap(bool bf16, int d_qk, int d_v, const CUtensorMap& q, const CUtensorMap& k,
+                              const CUtensorMap& v, const CUtensorMap& dout, const CUtensorMap& dq,
+                              const BwdParams& p, cudaStream_t st) {
+  if (bf16 && d_qk == 64 && d_v == 64) return launch_bwd_dq_cap_t<64, 64, true>(q, k, v, dout, dq, p, st);
+  if (!bf16 && d_qk == 64 && d_v == 64) return launch_bwd_dq_cap_t<64, 64, false>(q, k, v, dout, dq, p, st);
+  if (bf16 && d_qk == 128 && d_v == 128) return launch_bwd_dq_cap_t<128, 128, true>(q, k, v, dout, dq, p, st);
+  if (!bf16 && d_qk == 128 && d_v == 128) return launch_bwd_dq_cap_t<128, 128, false>(q, k, v, dout, dq, p, st);
+  if (bf16 && d_qk == 192 && d_v == 128) return launch_bwd_dq_cap_t<192, 128, true>(q, k, v, dout, dq, p, st);
+  if (!bf16 && d_qk == 192 && d_v == 128) return launch_bwd_dq_cap_t<192, 128, false>(q, k, v, dout, dq, p, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace sdpa

@@ -91,7 +91,7 @@ enum : int { QB_Q = 0, QB_KF, QB_KE = QB_KF + 2, QB_VF = QB_KE + 2, QB_VE = QB_V
 // DROP, BIAS and WIN (a local window or the bottom-right alignment) are
 // template parameters so the kernel without them is compiled alone and stays
 // within 96 registers a thread without spilling.
-template <int DQK, int DV, bool BF16, bool DROP, bool BIAS, bool WIN>
+template <int DQK, int DV, bool BF16, bool DROP, bool BIAS, bool WIN, bool CAP = false>
 __global__ void __launch_bounds__(DqCfg<DQK, DV>::THREADS, 1)
     sdpa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
@@ -456,6 +456,21 @@ __global__ void __launch_bounds__(DqCfg<DQK, DV>::THREADS, 1)
       }
       if (!(ok = mbar_wait(bar(QB_S), j & 1, ec, kSiteBwdCompute))) break;
       tc_fence_after();
+      if constexpr (CAP) {  // pr = P (1 - tanh^2); P itself is not needed here
+        tmem_ld32f(tbase + C::T_S + lane_off + CW * hf, pr);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(bar(QB_SFREE));
+        uint32_t pwc[16];
+        cap_probs<BF16>(pr, pwc, p.cap_in, p.cap_out, [&](int) { return make_float4(nl2, nl2, nl2, nl2); },
+                        [](int) { return 1.0f; });
+        const Band wb = lds_band(band_slot);
+        if ((kc0 + CW > S_kv) || (kc0 + CW - 1 > q0 + wb.hi) || (kc0 < q0 + BM - 1 + wb.lo) || !row_ok) {
+          const int first = qr + wb.lo;  // the row's visible keys, none past S_q
+          const int last = row_ok ? min(S_kv - 1, qr + wb.hi) : -1;
+          cap_mask(pr, pwc, [&](int c) { return kc0 + c < first || kc0 + c > last; });
+        }
+      } else {
       {
         uint32_t a0[32];
         tmem_ld32(tbase + C::T_S + lane_off + CW * hf, a0);
@@ -502,6 +517,7 @@ __global__ void __launch_bounds__(DqCfg<DQK, DV>::THREADS, 1)
       }
 #pragma unroll
       for (int c = 0; c < CW; ++c) pr[c] = ex2(pr[c]);
+      }
       const int b = j % C::DPB;  // dP buffer of this tile
       if (!(ok = mbar_wait(bar(QB_DP + b), (j / C::DPB) & 1, ec, kSiteBwdCompute))) break;
       tc_fence_after();
@@ -615,6 +631,18 @@ __global__ void __launch_bounds__(DqCfg<DQK, DV>::THREADS, 1)
   }
 }
 
+template <typename C, typename Kern>
+cudaError_t launch_dq_kernel(Kern kern, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                             const CUtensorMap& dout, const CUtensorMap& bias_map, const CUtensorMap& dq,
+                             const BwdParams& p, cudaStream_t st) {
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, 0);
+  if (e != cudaSuccess) return e;
+  const int n_qt = (p.S_q + C::BM - 1) / C::BM;
+  const long long grid = static_cast<long long>(n_qt) * p.B * p.H;
+  kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, st>>>(q, k, v, dout, bias_map, dq, p);
+  return cudaGetLastError();
+}
+
 template <int DQK, int DV, bool BF16>
 cudaError_t launch_bwd_dq_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                             const CUtensorMap& dout, const CUtensorMap& bias_map, const CUtensorMap& dq,
@@ -629,12 +657,18 @@ cudaError_t launch_bwd_dq_t(const CUtensorMap& q, const CUtensorMap& k, const CU
                              : sdpa_bwd_dq_kernel<DQK, DV, BF16, false, false, W>);
   };
   auto kern = (p.win_general || p.alibi != nullptr) ? pick(std::true_type{}) : pick(std::false_type{});
-  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, 0);
-  if (e != cudaSuccess) return e;
-  const int n_qt = (p.S_q + C::BM - 1) / C::BM;
-  const long long grid = static_cast<long long>(n_qt) * p.B * p.H;
-  kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, st>>>(q, k, v, dout, bias_map, dq, p);
-  return cudaGetLastError();
+  return launch_dq_kernel<C>(kern, q, k, v, dout, bias_map, dq, p, st);
+}
+
+// Capped scores (p.softcap > 0, no bias or ALiBi): the windowed kernel, which
+// also runs the plain masks.
+template <int DQK, int DV, bool BF16>
+cudaError_t launch_bwd_dq_cap_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                const CUtensorMap& dout, const CUtensorMap& dq, const BwdParams& p,
+                                cudaStream_t st) {
+  auto kern = p.dropout ? sdpa_bwd_dq_kernel<DQK, DV, BF16, true, false, true, true>
+                        : sdpa_bwd_dq_kernel<DQK, DV, BF16, false, false, true, true>;
+  return launch_dq_kernel<DqCfg<DQK, DV>>(kern, q, k, v, dout, CUtensorMap{}, dq, p, st);
 }
 
 }  // namespace sdpa

@@ -52,6 +52,9 @@ struct FwdParams {
   // Handled by the kernels compiled for general windows.
   const float* alibi;
   int alibi_stride, alibi_br;
+  // Capped scores (softcap > 0; see cap_r8): cap_in = 2 log2(e) scale / softcap
+  // and scale_log2 = -2 log2(e) softcap in that case.
+  float cap_in, softcap;
   const float* bias;       // [1, H, S_q, S_kv] fp32 or null
   int dropout;             // 0 / 1
   uint32_t drop_threshold; // drop iff draw < threshold
@@ -264,6 +267,9 @@ struct BwdParams {
   int H_kv;                // K/V heads; query head h reads K/V head h / (H / H_kv)
   float scale;             // softmax scale
   float scale_log2;        // scale * log2(e)
+  // Capped scores (softcap > 0; see cap_r8): cap_in as in FwdParams, cap_out =
+  // -2 log2(e) softcap, and the statistics hold -LSE log2(e) + log2(e) softcap.
+  float cap_in, cap_out, softcap;
   int win_left, win_right, win_br;  // visible keys, as in FwdParams
   int win_general;
   const float* alibi;      // ALiBi slopes, as in FwdParams
@@ -412,6 +418,47 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Capped scores: S'' = cap tanh(S' / cap), S' = scale S. With
+//   r = 1 / (1 + e^(2 S' / cap)):   tanh(S' / cap) = 1 - 2 r,
+//   S'' = cap - 2 cap r,            1 - tanh^2 = 4 r (1 - r),
+// so r is all the kernels need: the exponent of the softmax is one FMA of it,
+// and the backward's factor keeps its relative precision where tanh saturates.
+// Takes x[0, 8) raw scores S to r, c = 2 log2(e) scale / cap. The exponential
+// unit bounds these kernels, so four values share one reciprocal: with
+// a_i = 1 + e_i, 1 / a_0 = a_1 (a_2 a_3) / (a_0 a_1 a_2 a_3) and so on (2.25
+// multiplies and a quarter of a reciprocal a value). The exponent is held to
+// 30 so that the product of four stays below 2^121; there r is under 2^-29
+// and S'' within cap 2^-29 of the cap. r is off by at most about 2^-21
+// relative (two approximate functions and six roundings), S'' by cap 2^-21.
+// tanh.approx would take one exponential unit slot less a value and leave
+// S'' off by cap 2^-11, which at a cap of 50 is 2.4% of P.
+__device__ __forceinline__ void cap_r8(float* x, float c) {
+  const uint64_t c2 = f2(c, c), one = f2(1.f, 1.f);
+  uint64_t a[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = f2split(mul2(f2(x[2 * i], x[2 * i + 1]), c2));
+    a[i] = add2(f2(ex2(fminf(y.x, 30.f)), ex2(fminf(y.y, 30.f))), one);
+  }
+  const uint64_t p01 = mul2(a[0], a[1]), p23 = mul2(a[2], a[3]);
+  const float2 all = f2split(mul2(p01, p23));
+  const uint64_t inv = f2(rcp(all.x), rcp(all.y));
+  const uint64_t i01 = mul2(inv, p23), i23 = mul2(inv, p01);
+  const uint64_t r[4] = {mul2(i01, a[1]), mul2(i01, a[0]), mul2(i23, a[3]), mul2(i23, a[2])};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = f2split(r[i]);
+    x[2 * i] = v.x;
+    x[2 * i + 1] = v.y;
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (BF16) {
@@ -432,6 +479,47 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     __half2 v = *reinterpret_cast<__half2*>(&w);
     return __half22float2(v);
   }
+}
+
+// Capped scores, backward: raw scores s[0, 32) of one thread's columns to P
+// and P (1 - tanh^2). The exponent is cap_out r + n (n: the statistic, which
+// holds -LSE log2e + softcap log2e), 1 - tanh^2 = 4 r (1 - r). P leaves
+// packed for the dV product (times the dropout factor zf), so that the
+// fp32 registers hold only P (1 - tanh^2), which the softmax backward
+// multiplies by dP - D. Columns outside [first, lim) are masked to zero by
+// selection: P of a hidden score may be infinite.
+template <bool BF16, typename Stat, typename Zf>
+__device__ __forceinline__ void cap_probs(float (&s)[32], uint32_t (&pw)[16], float cap_in, float cap_out,
+                                          Stat stat4, Zf zf) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) cap_r8(s + i, cap_in);
+  const uint64_t co2 = f2(cap_out, cap_out), four = f2(4.f, 4.f), mfour = f2(-4.f, -4.f);
+#pragma unroll
+  for (int e4 = 0; e4 < 8; ++e4) {
+    const float4 n4 = stat4(e4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = 4 * e4 + 2 * h;
+      const uint64_t r = f2(s[c], s[c + 1]);
+      const float2 x = f2split(fma2(r, co2, h ? f2(n4.z, n4.w) : f2(n4.x, n4.y)));
+      const float p0 = ex2(x.x), p1 = ex2(x.y);
+      pw[c / 2] = pack2<BF16>(p0 * zf(c), p1 * zf(c + 1));
+      const float2 g = f2split(mul2(f2(p0, p1), mul2(r, fma2(r, mfour, four))));
+      s[c] = g.x;
+      s[c + 1] = g.y;
+    }
+  }
+}
+
+// Zeroes columns c of both where hidden(c).
+template <typename Hidden>
+__device__ __forceinline__ void cap_mask(float (&s)[32], uint32_t (&pw)[16], Hidden hidden) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (hidden(c)) {
+      s[c] = 0.f;
+      pw[c / 2] &= (c & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+    }
 }
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
@@ -505,11 +593,27 @@ cudaError_t launch_bwd_fused_bf16(int d_qk, int d_v, const CUtensorMap& q, const
 cudaError_t launch_bwd_fused_fp16(int d_qk, int d_v, const CUtensorMap& q, const CUtensorMap& k,
                                   const CUtensorMap& v, const CUtensorMap& dout, const CUtensorMap& dk,
                                   const CUtensorMap& dv, const BwdParams& p, cudaStream_t st);
+// The capped-score forms (softcap > 0, no bias or ALiBi); bf16 or fp16.
+cudaError_t launch_fwd_cap(bool bf16, int d_qk, int d_v, const CUtensorMap& q, const CUtensorMap& k,
+                           const CUtensorMap& v, const FwdParams& p, cudaStream_t st);
+cudaError_t launch_bwd_dkdv_cap_bf16(int d_qk, int d_v, const CUtensorMap& q, const CUtensorMap& k,
+                                     const CUtensorMap& v, const CUtensorMap& dout, const CUtensorMap& dk,
+                                     const CUtensorMap& dv, const BwdParams& p, cudaStream_t st);
+cudaError_t launch_bwd_dkdv_cap_fp16(int d_qk, int d_v, const CUtensorMap& q, const CUtensorMap& k,
+                                     const CUtensorMap& v, const CUtensorMap& dout, const CUtensorMap& dk,
+                                     const CUtensorMap& dv, const BwdParams& p, cudaStream_t st);
+cudaError_t launch_bwd_dq_cap(bool bf16, int d_qk, int d_v, const CUtensorMap& q, const CUtensorMap& k,
+                              const CUtensorMap& v, const CUtensorMap& dout, const CUtensorMap& dq,
+                              const BwdParams& p, cudaStream_t st);
+cudaError_t launch_bwd_fused_cap(bool bf16, int d_qk, int d_v, const CUtensorMap& q, const CUtensorMap& k,
+                                 const CUtensorMap& v, const CUtensorMap& dout, const CUtensorMap& dk,
+                                 const CUtensorMap& dv, const BwdParams& p, cudaStream_t st);
+// lse_shift: added to every finite -LSE log2(e) (capped scores: log2(e) softcap)
 cudaError_t launch_bwd_pre(bool bf16, const void* o, const void* dout, const float* lse, float* stats,
                            float* dbias, int64_t z_count, int s_q, int s_pad, int rows,
                            const int* seqstart, int n_seq, int d_v, int64_t dbias_elems,
                            int* counters, int n_counters, float* dq_acc, int64_t dq_acc_elems,
-                           cudaStream_t st);
+                           float lse_shift, cudaStream_t st);
 cudaError_t launch_dq_convert(bool bf16, const float* dq_acc, void* dq, int64_t z_count, int rows,
                               int dq_tiles, int d_qk, float scale, cudaStream_t st);
 cudaError_t launch_dropout_mask(int64_t total, uint32_t threshold, uint32_t seed_lo,

@@ -86,7 +86,7 @@ struct FwdCfg {
 enum : int { FB_Q = 0, FB_S, FB_P = FB_S + 2, FB_O = FB_P + 2, FB_DRAIN = FB_O + 2, FB_KF,
              FB_KE = FB_KF + 3, FB_VF = FB_KE + 3, FB_VE = FB_VF + 3, FB_COUNT = FB_VE + 3 };
 
-template <int DQK, int DV, bool BF16, bool GENERAL, bool WIN, bool RAW, bool DROP>
+template <int DQK, int DV, bool BF16, bool GENERAL, bool WIN, bool RAW, bool DROP, bool CAP = false>
 __global__ void __launch_bounds__(384, 1)
     sdpa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -347,8 +347,12 @@ __global__ void __launch_bounds__(384, 1)
     // -inf, the row max is the largest raw score (the smallest under a
     // negative scale) times scale * log2e, which equals the largest scaled
     // score since rounding is monotonic, and P = 2^fma(S, scale * log2e, -m).
+    // CAP (capped scores): the raw score is cap_r8's r, whose exponent scale
+    // sl2 = -2 softcap log2e is negative; the cap itself, which every score
+    // has, cancels in P and joins the LSE at the end.
     static_assert(!(RAW && GENERAL), "raw scores have no additive terms");
-    const float neg = (RAW && sl2 < 0.f) ? -SDPA_NEG_INF : SDPA_NEG_INF;  // masked score
+    static_assert(!CAP || RAW, "capped scores take the raw path");
+    const float neg = (CAP || (RAW && sl2 < 0.f)) ? -SDPA_NEG_INF : SDPA_NEG_INF;  // masked score
     float m = SDPA_NEG_INF, l = 0.f;
     bool ok = true;
     for (int c = 0; c < n_kv; ++c) {
@@ -432,6 +436,10 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32f(tS + lane_off + q * 32, x + q * 32);
         tmem_wait_ld();
+        if constexpr (CAP) {
+#pragma unroll
+          for (int i = 0; i < 128; i += 8) cap_r8(x + i, p.cap_in);
+        }
         if constexpr (!RAW) {
 #pragma unroll
           for (int i = 0; i < 128; i += 2) {
@@ -465,7 +473,7 @@ __global__ void __launch_bounds__(384, 1)
           if (k0 + i > lim) x[i] = neg;
       }
       float mx;
-      if (!RAW || sl2 > 0.f) {
+      if (!CAP && (!RAW || sl2 > 0.f)) {
         mx = extreme_of<false, 128>(x);
         if (RAW) mx *= sl2;
       } else {
@@ -552,7 +560,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (row_ok)
-        p.lse[ri] = (l > 0.f) ? fmaf(m, kLn2, __logf(l)) : SDPA_NEG_INF;
+        p.lse[ri] = (l > 0.f) ? fmaf(m, kLn2, __logf(l)) + (CAP ? p.softcap : 0.f) : SDPA_NEG_INF;
     } else if (n_kv == 0 && row_ok && !(t == 1 && lone)) {
       // no row of this tile sees a key (the other tile's rows do): O = 0, LSE = -inf
       // (a lone tile 0's partner rows belong to the next pair)
@@ -570,6 +578,20 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc(tbase, C::TMEM_COLS);
   }
+}
+
+template <typename C, typename Kern>
+cudaError_t launch_fwd_kernel(Kern kern, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                              const FwdParams& p, cudaStream_t st) {
+  // The warpgroups' setmaxnreg shares add up to exactly 384 x REG_LAUNCH; had
+  // the compiler given the kernel another launch register count, the softmax
+  // warpgroups' increase could never be granted, so refuse to launch then.
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, C::REG_LAUNCH);
+  if (e != cudaSuccess) return e;
+  const int n_qt = (p.S_q + C::BM - 1) / C::BM;
+  const long long grid = static_cast<long long>((n_qt + 1) / 2) * p.B * p.H;
+  kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, st>>>(q, k, v, p);
+  return cudaGetLastError();
 }
 
 template <int DQK, int DV, bool BF16>
@@ -590,15 +612,17 @@ cudaError_t launch_fwd_t(const CUtensorMap& q, const CUtensorMap& k, const CUten
                                  : sdpa_fwd_kernel<DQK, DV, BF16, false, false, true, D>);
   };
   auto kern = p.dropout ? pick(std::true_type{}) : pick(std::false_type{});
-  // The warpgroups' setmaxnreg shares add up to exactly 384 x REG_LAUNCH; had
-  // the compiler given the kernel another launch register count, the softmax
-  // warpgroups' increase could never be granted, so refuse to launch then.
-  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, C::REG_LAUNCH);
-  if (e != cudaSuccess) return e;
-  const int n_qt = (p.S_q + C::BM - 1) / C::BM;
-  const long long grid = static_cast<long long>((n_qt + 1) / 2) * p.B * p.H;
-  kern<<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, st>>>(q, k, v, p);
-  return cudaGetLastError();
+  return launch_fwd_kernel<C>(kern, q, k, v, p, st);
+}
+
+// Capped scores (p.softcap > 0, no bias or ALiBi): the windowed raw-score
+// kernel, which also runs the plain masks.
+template <int DQK, int DV, bool BF16>
+cudaError_t launch_fwd_cap_t(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                             const FwdParams& p, cudaStream_t st) {
+  auto kern = p.dropout ? sdpa_fwd_kernel<DQK, DV, BF16, false, true, true, true, true>
+                        : sdpa_fwd_kernel<DQK, DV, BF16, false, true, true, false, true>;
+  return launch_fwd_kernel<FwdCfg<DQK, DV>>(kern, q, k, v, p, st);
 }
 
 }  // namespace sdpa
