@@ -432,6 +432,72 @@ sdpa_status_t sdpa_bwd_phases_varlen_capped(
     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Norms of queries and keys for each head with the position rotation, from
+ * the projection's layout to the attention's, one pass for queries, keys and
+ * (as a change of layout alone) values. Per row x of d elements:
+ *     u = x * (mean(x^2) + eps)^(-1/2) * weight   (u = x with a null weight)
+ *     y = u with its first `rot` elements turned in pairs:
+ *         (u_i, u_j) -> (u_i c - u_j s, u_j c + u_i s),
+ *         (i, j) = (m, m + rot/2), or (2m, 2m + 1) when `interleaved`, with
+ *         c, s = cos, sin[position][m], m < rot/2
+ * in fp32, rounded once; the values' bits are copied.
+ *   sdpa_rows_t  rows of a 4-D tensor: device pointer and the element strides
+ *            of batch, row (token) and head; a row's elements are contiguous.
+ *            Pointers and the strides of dimensions of more than one element
+ *            must be multiples of 16 bytes (SDPA_ERR_MISALIGNED). Outputs
+ *            must overlap neither inputs nor each other.
+ *   Inputs   q [b, s, h, d], k [b, s, h_kv, d], v [b, s, h_kv, d_v] (v and
+ *            v_out null: no values), as sdpa_rows_t {batch, token, head}, e.g.
+ *            slices of one fused projection. d in {64, 128, 192}, d_v in the
+ *            same and at most d. h and h_kv need no common factor.
+ *   Outputs  q_out [b, h, s, d], k_out [b, h_kv, s, d], v_out [b, h_kv, s, d_v].
+ *            With kv_rows (device int32 [b]) k_out and v_out are caches
+ *            [b, h_kv, cache_rows, d]: token t of sequence i goes to row
+ *            kv_rows[i] + t, and is dropped when that is outside
+ *            [0, cache_rows). No other row is touched.
+ *   rot      multiple of 16, 0 (no rotation) to d.
+ *   cos, sin fp32 [n_pos, rot / 2], 16-byte aligned. positions: device int32
+ *            [b, s], or null: token t has position t (n_pos >= s then). A
+ *            position outside [0, n_pos) takes the nearest one's angles.
+ *   weights  [d] in the io type, or fp32 when weight_fp32 is set, 16-byte
+ *            aligned; null: that side is not normalised.
+ *   eps      positive and finite.
+ * The backward takes the gradients of the outputs in the attention's layout
+ * and the forward's inputs q, k (null where there is no weight), and writes
+ * dq, dk, dv in the projection's layout (any strides) and dq_weight,
+ * dk_weight ([d], the weights' type; null where there is no weight), summed
+ * over all rows in fp32 in an order that depends on the sizes alone, so they
+ * are reproducible bit for bit. dq, dk may be the storage of dq_out, dk_out
+ * in no case. Workspace: 256-byte aligned, of the size given, with a weight.
+ * b or s of 0: a no-op (the weight gradients become 0).
+ */
+typedef struct {
+  void* ptr;
+  int64_t batch_stride, row_stride, head_stride;
+} sdpa_rows_t;
+sdpa_status_t sdpa_qk_norm_rope(int64_t b, int64_t s, int64_t h, int64_t h_kv, int64_t d, int64_t d_v,
+                                sdpa_dtype_t dtype, const sdpa_rows_t* q, const sdpa_rows_t* k,
+                                const sdpa_rows_t* v, const sdpa_rows_t* q_out,
+                                const sdpa_rows_t* k_out, const sdpa_rows_t* v_out, int64_t rot,
+                                int interleaved, const float* cos, const float* sin, int64_t n_pos,
+                                const int32_t* positions, const void* q_weight,
+                                const void* k_weight, int weight_fp32, float eps,
+                                const int32_t* kv_rows, int64_t cache_rows, void* stream);
+size_t sdpa_qk_norm_rope_bwd_workspace_size(int64_t b, int64_t s, int64_t h, int64_t h_kv, int64_t d,
+                                            int64_t d_v);
+sdpa_status_t sdpa_qk_norm_rope_bwd(int64_t b, int64_t s, int64_t h, int64_t h_kv, int64_t d,
+                                    int64_t d_v, sdpa_dtype_t dtype, const sdpa_rows_t* dq_out,
+                                    const sdpa_rows_t* dk_out, const sdpa_rows_t* dv_out,
+                                    const sdpa_rows_t* q, const sdpa_rows_t* k,
+                                    const sdpa_rows_t* dq, const sdpa_rows_t* dk,
+                                    const sdpa_rows_t* dv, int64_t rot, int interleaved,
+                                    const float* cos, const float* sin, int64_t n_pos,
+                                    const int32_t* positions, const void* q_weight,
+                                    const void* k_weight, int weight_fp32, float eps,
+                                    void* dq_weight, void* dk_weight, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
  * The backward pass for callers that cannot allocate device memory when they
  * run it (a host framework that owns all GPU memory through its own pool, or
  * a latency-critical loop that cannot afford cudaMalloc's implicit

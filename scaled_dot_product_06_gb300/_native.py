@@ -28,6 +28,14 @@ SDPA_FP16 = 1
 # name -> (restype, argtypes), in the order of include/sdpa.h
 _i64, _f32, _int, _u64, _ptr, _sz = (ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_uint64,
                                      ctypes.c_void_p, ctypes.c_size_t)
+
+
+class Rows(ctypes.Structure):  # sdpa_rows_t
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch_stride", _i64), ("row_stride", _i64),
+                ("head_stride", _i64)]
+
+
+_rows = _ptr  # a Rows by reference, or its bytes
 SIGNATURES = {
     "sdpa_fwd": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _f32, _int, _f32, _u64, _u64, _int,
                         _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr]),
@@ -86,6 +94,13 @@ SIGNATURES = {
                                              _f32, _i64, _i64, _int, _ptr, _f32, _u64, _u64, _int, _ptr, _ptr,
                                              _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _sz,
                                              _ptr]),
+    "sdpa_qk_norm_rope": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _int, _rows, _rows, _rows, _rows, _rows,
+                                 _rows, _i64, _int, _ptr, _ptr, _i64, _ptr, _ptr, _ptr, _int, _f32, _ptr,
+                                 _i64, _ptr]),
+    "sdpa_qk_norm_rope_bwd_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64]),
+    "sdpa_qk_norm_rope_bwd": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _int, _rows, _rows, _rows, _rows,
+                                     _rows, _rows, _rows, _rows, _i64, _int, _ptr, _ptr, _i64, _ptr, _ptr,
+                                     _ptr, _int, _f32, _ptr, _ptr, _ptr, _sz, _ptr]),
     "sdpa_bwd_noalloc": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _f32, _int, _f32, _u64, _u64,
                                 _int, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr,
                                 _ptr, _ptr]),
