@@ -498,6 +498,37 @@ sdpa_status_t sdpa_qk_norm_rope_bwd(int64_t b, int64_t s, int64_t h, int64_t h_k
                                     size_t workspace_bytes, void* stream);
 
 /*
+ * Attention of a batch's new tokens over a prefix that the whole batch shares,
+ * read once for all, and over each sequence's own keys behind it (the forward
+ * of a decoding step, or of a few drafted tokens).
+ *   q, o     [b, h, s_q, d]; lse fp32 [b, h, s_q], as in sdpa_fwd.
+ *   k_prefix, v_prefix  [h_kv, s_prefix, d]: the shared keys and values. May
+ *            be null when s_prefix is 0 (then a plain decoding step).
+ *   k, v     [b, h_kv, s_max, d]: each sequence's cache. Null when s_max is 0.
+ *   seqlen_k DEVICE int32 [b] (4-byte aligned): own keys of each sequence, the
+ *            s_q new tokens' among them (appended beforehand); read on the
+ *            device and held in [0, s_max]. Rows behind them may hold
+ *            anything, NaN too. New token t sees the whole prefix and own keys
+ *            j <= seqlen_k - s_q + t. A row that sees no key gets O = 0 and
+ *            LSE = -inf.
+ *   scale    as in sdpa_fwd; softcap 0 (none) or as in the capped calls.
+ *   Heads    h_kv divides h; query head i reads K/V head i / (h / h_kv).
+ *   Layout   contiguous, pointers 16-byte aligned, head sizes as elsewhere.
+ *   Workspace  sdpa_fwd_prefix_workspace_size(...) bytes, 256-byte aligned:
+ *            fp32 partial rows of the key ranges the work is cut into. Two
+ *            calls that may run at the same time need one each.
+ * Results are the same bits in every run. b, h or s_q of 0: a no-op.
+ */
+size_t sdpa_fwd_prefix_workspace_size(int64_t b, int64_t h, int64_t h_kv, int64_t s_q,
+                                      int64_t s_prefix, int64_t s_max, int64_t d_qk, int64_t d_v);
+sdpa_status_t sdpa_fwd_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t s_prefix,
+                              int64_t s_max, int64_t d_qk, int64_t d_v, float scale, float softcap,
+                              sdpa_dtype_t dtype, const void* q, const void* k_prefix,
+                              const void* v_prefix, const void* k, const void* v,
+                              const int32_t* seqlen_k, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
  * The backward pass for callers that cannot allocate device memory when they
  * run it (a host framework that owns all GPU memory through its own pool, or
  * a latency-critical loop that cannot afford cudaMalloc's implicit

@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libsdpa.so")
 SOURCES = ["api.cu", "aux.cu", "noalloc.cu", "fwd_bf16.cu", "fwd_fp16.cu", "bwd_dkdv_bf16.cu",
            "bwd_dkdv_fp16.cu", "bwd_dq_bf16.cu", "bwd_dq_fp16.cu", "bwd_fused_bf16.cu",
            "bwd_fused_fp16.cu", "fwd_cap.cu", "bwd_dkdv_cap_bf16.cu", "bwd_dkdv_cap_fp16.cu",
-           "bwd_dq_cap.cu", "bwd_fused_cap.cu", "norm_rope.cu", "norm_rope_api.cu"]
+           "bwd_dq_cap.cu", "bwd_fused_cap.cu", "norm_rope.cu", "norm_rope_api.cu",
+           "prefix_bf16.cu", "prefix_fp16.cu", "prefix_join.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

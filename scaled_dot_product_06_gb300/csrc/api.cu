@@ -4,6 +4,7 @@
 // flag, dropout probability with seed and offset, optional bias, fp32 softmax
 // statistics) with plain pointers and a status return instead of exceptions,
 // the way oneDNN's sdpa micro.cpp reports failures through status codes.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -16,6 +17,7 @@
 
 #include "../../include/sdpa.h"
 #include "common.cuh"
+#include "prefix.cuh"
 
 namespace {
 
@@ -746,9 +748,162 @@ sdpa_status_t bwd_impl(int phases, int64_t b, int64_t h, int64_t h_kv, int64_t s
   return SDPA_OK;
 }
 
+// ---------------------------------------------------------------- shared prefix
+// Map over q's rows as [K/V head][sequence][R rows][d]: one box holds 64 columns
+// of `rows` rows of each of `seqs` sequences.
+sdpa_status_t encode_rows_map(CUtensorMap* m, CUtensorMapDataType type, const void* q, int64_t d, int64_t R,
+                              int64_t b, int64_t h_kv, uint32_t rows, uint32_t seqs) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  if (sdpa_status_t s = encoder(&enc)) return s;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(R), static_cast<cuuint64_t>(b),
+                        static_cast<cuuint64_t>(h_kv)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(d * 2), static_cast<cuuint64_t>(h_kv * R * d * 2),
+                           static_cast<cuuint64_t>(R * d * 2)};
+  cuuint32_t box[4] = {64, rows, seqs, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, type, 4, const_cast<void*>(q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled (rows) failed (CUresult %d)",
+             static_cast<int>(r));
+    return SDPA_ERR_CUDA;
+  }
+  return SDPA_OK;
+}
+
+// Sizes of a shared-prefix call, and its work items: both key sets are cut
+// into chunks of c key tiles, c such that there are about two items an SM (one
+// tile at least). Fewer, longer items leave SMs idle at the end; more add
+// partial rows, 4 (d_v + 1) bytes each written and read.
+sdpa_status_t plan_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t s_prefix, int64_t s_max,
+                          int64_t d_qk, int64_t d_v, PrefixParams* p, bool* empty, size_t* bytes) {
+  if (sdpa_status_t s = check_sizes(b, h, s_q, s_prefix, d_qk, d_v, 0.f, SDPA_BF16, empty)) return s;
+  if (s_max < 0) return fail(SDPA_ERR_INVALID_ARG, "s_max");
+  if (s_max > kMaxSeq) return fail(SDPA_ERR_UNSUPPORTED, "s_max");
+  if (!kv_heads_ok(h, h_kv)) return fail(SDPA_ERR_INVALID_ARG, "h_kv must divide h");
+  *empty = b == 0 || h == 0 || s_q == 0;
+  *bytes = 0;
+  if (*empty) return SDPA_OK;
+  const int64_t R = h / h_kv * s_q, rows = b * h * s_q;
+  if (rows > (int64_t{1} << 30)) return fail(SDPA_ERR_UNSUPPORTED, "too many query rows");
+  p->B = static_cast<int>(b);
+  p->H_kv = static_cast<int>(h_kv);
+  p->R = static_cast<int>(R);
+  p->s_q = static_cast<int>(s_q);
+  p->s_prefix = static_cast<int>(s_prefix);
+  p->s_max = static_cast<int>(s_max);
+  p->rows = rows;
+  const int64_t seqs = R <= 128 ? std::min<int64_t>(128 / R, b) : 1, per = (R + 127) / 128;
+  p->seqs_tile = static_cast<int>(seqs);
+  const int64_t tiles_p = R <= 128 ? (b + seqs - 1) / seqs : b * per;
+  p->row_tiles_p = static_cast<int>(tiles_p);
+  p->row_tiles_o = static_cast<int>(per);
+  p->dual_p = tiles_p > 1;
+  p->dual_o = per > 1;
+  const int64_t blocks_p = p->dual_p ? (tiles_p + 1) / 2 : 1, blocks_o = p->dual_o ? (per + 1) / 2 : 1;
+  p->row_blocks_p = static_cast<int>(blocks_p);
+  p->row_blocks_o = static_cast<int>(blocks_o);
+  const int64_t kt_p = (s_prefix + 127) / 128, kt_o = (s_max + 127) / 128;
+  const int64_t items_p = blocks_p * h_kv, items_o = blocks_o * b * h_kv;
+  const double visits = static_cast<double>(items_p) * kt_p + static_cast<double>(items_o) * kt_o;
+  const int64_t c = std::max<int64_t>(1, static_cast<int64_t>(std::ceil(visits / (2 * 152))));
+  p->chunk_p = static_cast<int>(std::max<int64_t>(1, std::min(c, kt_p)));
+  p->chunk_o = static_cast<int>(std::max<int64_t>(1, std::min(c, kt_o)));
+  const int64_t sp = (kt_p + p->chunk_p - 1) / p->chunk_p, so = (kt_o + p->chunk_o - 1) / p->chunk_o;
+  if (items_p * sp + items_o * so > (int64_t{1} << 30)) return fail(SDPA_ERR_UNSUPPORTED, "too many work items");
+  p->splits_p = static_cast<int>(sp);
+  p->splits_o = static_cast<int>(so);
+  p->items_prefix = static_cast<int>(items_p * sp);
+  p->items_own = static_cast<int>(items_o * so);
+  p->slots_p = static_cast<int>(sp * (p->dual_p ? 1 : 2));
+  p->slots_o = static_cast<int>(so * (p->dual_o ? 1 : 2));
+  p->q_box_p = static_cast<uint32_t>(128 * std::min<int64_t>(R, 128) * seqs);
+  p->q_box_o = static_cast<uint32_t>(128 * std::min<int64_t>(R, 128));
+  // partial rows, then their log-sums
+  *bytes = (static_cast<size_t>(p->slots_p + p->slots_o) * rows * (d_v + 1) * sizeof(float) + 255) & ~size_t(255);
+  return SDPA_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t sdpa_fwd_prefix_workspace_size(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t s_prefix,
+                                      int64_t s_max, int64_t d_qk, int64_t d_v) {
+  PrefixParams p{};
+  bool empty = false;
+  size_t bytes = 0;
+  if (plan_prefix(b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v, &p, &empty, &bytes) != SDPA_OK) return 0;
+  return bytes;
+}
+
+sdpa_status_t sdpa_fwd_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t s_prefix, int64_t s_max,
+                              int64_t d_qk, int64_t d_v, float scale, float softcap, sdpa_dtype_t dtype,
+                              const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                              const void* v, const int32_t* seqlen_k, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  PrefixParams p{};
+  bool empty = false;
+  size_t need = 0;
+  if (dtype != SDPA_BF16 && dtype != SDPA_FP16) return fail(SDPA_ERR_UNSUPPORTED, "dtype");
+  if (sdpa_status_t s = plan_prefix(b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v, &p, &empty, &need)) return s;
+  if (!scale_ok(scale)) return fail(SDPA_ERR_INVALID_ARG, "scale must be finite");
+  Mask cap{-1, -1, 0};
+  cap.capped = softcap != 0.f;
+  cap.softcap = softcap;
+  if (sdpa_status_t s = check_softcap(cap, scale)) return s;
+  if (empty) return SDPA_OK;
+  if (!q || !o || !lse || (s_prefix > 0 && (!k_prefix || !v_prefix)) || (s_max > 0 && (!k || !v || !seqlen_k)))
+    return fail(SDPA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(q) || !aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(seqlen_k) & 3u) != 0)
+    return SDPA_ERR_MISALIGNED;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SDPA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SDPA_ERR_MISALIGNED;
+
+  if (softcap != 0.f) {
+    p.cap_in = 2.f * kLog2e * scale / softcap;
+    p.scale_log2 = -2.f * kLog2e * softcap;
+    p.lse_shift = kLog2e * softcap;
+  } else if (scale == 0.f) {
+    // every score 0: the capped form with a cap of 1 (the plain one masks raw
+    // scores with infinities, which a zero factor would turn into NaN)
+    p.scale_log2 = -2.f * kLog2e;
+    p.lse_shift = kLog2e;
+  } else {
+    p.scale_log2 = scale * kLog2e;
+  }
+  p.seqlen = seqlen_k;
+  p.part = static_cast<float*>(workspace);
+  p.part_lse = p.part + static_cast<int64_t>(p.slots_p + p.slots_o) * p.rows * d_v;
+  p.o = o;
+  p.lse = lse;
+  const bool bf16 = dtype == SDPA_BF16;
+  const CUtensorMapDataType tt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p.items_prefix + p.items_own > 0) {
+    CUtensorMap m[6] = {};
+    const uint32_t box = static_cast<uint32_t>(std::min(p.R, 128));
+    if (p.items_prefix > 0) {
+      if (sdpa_status_t s = encode_rows_map(&m[0], tt, q, d_qk, p.R, b, h_kv, box,
+                                            static_cast<uint32_t>(p.seqs_tile)))
+        return s;
+      if (sdpa_status_t s = make_map(&m[2], tt, 2, k_prefix, d_qk, s_prefix, h_kv, 128, true)) return s;
+      if (sdpa_status_t s = make_map(&m[3], tt, 2, v_prefix, d_v, s_prefix, h_kv, 128, true)) return s;
+    }
+    if (p.items_own > 0) {
+      if (sdpa_status_t s = encode_rows_map(&m[1], tt, q, d_qk, p.R, b, h_kv, box, 1)) return s;
+      if (sdpa_status_t s = make_map(&m[4], tt, 2, k, d_qk, s_max, b * h_kv, 128, true)) return s;
+      if (sdpa_status_t s = make_map(&m[5], tt, 2, v, d_v, s_max, b * h_kv, 128, true)) return s;
+    }
+    if (sdpa_status_t s = error_word_ptr(&p.err)) return s;
+    const int di = static_cast<int>(d_qk), dvi = static_cast<int>(d_v);
+    const cudaError_t e = bf16 ? launch_prefix_bf16(di, dvi, m, p, st) : launch_prefix_fp16(di, dvi, m, p, st);
+    if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "shared-prefix kernel launch", e);
+  }
+  return cuda_status(launch_prefix_join(bf16, static_cast<int>(d_v), p, st), "partial join launch");
+}
 
 const char* sdpa_status_string(sdpa_status_t s) {
   switch (s) {
