@@ -389,16 +389,25 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// The same, but not a number where one of them is not.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float fmin3(float a, float b, float c) {
   float d;
   asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // Largest (MIN: smallest) of x[0, N), N a multiple of 8, in four chains.
-template <bool MIN, int N>
+// (NAN_TOO: not a number where one of them is not.)
+template <bool MIN, int N, bool NAN_TOO = false>
 __device__ __forceinline__ float extreme_of(const float* x) {
-  static_assert(N % 8 == 0, "extreme_of");
-  auto f3 = [](float a, float b, float c) { return MIN ? fmin3(a, b, c) : fmax3(a, b, c); };
+  static_assert(N % 8 == 0 && !(MIN && NAN_TOO), "extreme_of");
+  auto f3 = [](float a, float b, float c) {
+    return MIN ? fmin3(a, b, c) : NAN_TOO ? fmax3_nan(a, b, c) : fmax3(a, b, c);
+  };
   float a0 = x[0], a1 = x[1], a2 = x[2], a3 = x[3];
 #pragma unroll
   for (int i = 4; i < N - 4; i += 8) {
@@ -437,14 +446,21 @@ __device__ __forceinline__ float rcp(float x) {
 // and S'' within cap 2^-29 of the cap. r is off by at most about 2^-21
 // relative (two approximate functions and six roundings), S'' by cap 2^-21.
 // tanh.approx would take one exponential unit slot less a value and leave
-// S'' off by cap 2^-11, which at a cap of 50 is 2.4% of P.
+// S'' off by cap 2^-11, which at a cap of 50 is 2.4% of P. An odd polynomial
+// of S' / cap up to 3/4 (four FMAs and a multiply, no exponential unit) did
+// not pay: the softmax warps wait for their own instructions, not for that
+// unit (38% busy), and b4 h16 s2048 d128 took 111 us causal for 108.
+// HOLD: with the hold at 30; there a score that is not a number counts as a
+// large one (the backward has such a row's statistics, which are none either).
+template <bool HOLD = true>
 __device__ __forceinline__ void cap_r8(float* x, float c) {
+  auto held = [](float y) { return HOLD ? fminf(y, 30.f) : y; };
   const uint64_t c2 = f2(c, c), one = f2(1.f, 1.f);
   uint64_t a[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 y = f2split(mul2(f2(x[2 * i], x[2 * i + 1]), c2));
-    a[i] = add2(f2(ex2(fminf(y.x, 30.f)), ex2(fminf(y.y, 30.f))), one);
+    a[i] = add2(f2(ex2(held(y.x)), ex2(held(y.y))), one);
   }
   const uint64_t p01 = mul2(a[0], a[1]), p23 = mul2(a[2], a[3]);
   const float2 all = f2split(mul2(p01, p23));
@@ -457,6 +473,32 @@ __device__ __forceinline__ void cap_r8(float* x, float c) {
     x[2 * i] = v.x;
     x[2 * i + 1] = v.y;
   }
+}
+
+// The forward's raw scores x[0, N) of a row to r; returns the largest log2
+// score of all of them (relative to the cap, as sl2 r), for tiles without a
+// hidden key. One pass for the largest raw score, three values an instruction,
+// shows whether the hold at 30 is needed and whether a score is not a number,
+// and costs less than the holds. Such a score stays one, and alone: hidden
+// keys may hold anything.
+template <int N>
+__device__ __forceinline__ float cap_scores(float* x, float c, float sl2) {
+  const float hi = extreme_of<false, N, true>(x);
+  if (__all_sync(0xffffffffu, c > 0.f && hi * c <= 30.f)) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) cap_r8<false>(x + i, c);
+    return sl2 * rcp(1.f + ex2(hi * c));
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = x[i + e];
+    cap_r8(r, c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[i + e] = x[i + e] == x[i + e] ? r[e] : x[i + e];
+  }
+  return sl2 * extreme_of<true, N>(x);
 }
 
 template <bool BF16>

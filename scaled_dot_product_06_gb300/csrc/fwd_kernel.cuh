@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(384, 1)
     // sl2 = -2 softcap log2e is negative; the cap itself, which every score
     // has, cancels in P and joins the LSE at the end.
     static_assert(!(RAW && GENERAL), "raw scores have no additive terms");
-    static_assert(!CAP || RAW, "capped scores take the raw path");
+    static_assert(!CAP || (RAW && WIN), "capped scores take the raw path and the mask's general form");
     const float neg = (CAP || (RAW && sl2 < 0.f)) ? -SDPA_NEG_INF : SDPA_NEG_INF;  // masked score
     float m = SDPA_NEG_INF, l = 0.f;
     bool ok = true;
@@ -359,6 +359,8 @@ __global__ void __launch_bounds__(384, 1)
       const int k0 = (khi_t - c) * C::BN;  // key tiles from the diagonal down
       // scores in the log2 domain: S * scale * log2e (+ Bias * log2e)
       float x[128];
+      float mx = SDPA_NEG_INF;  // the row's largest score of the tile
+      bool hidden = false;      // the tile has hidden keys
       if (GENERAL && bias_row != nullptr) {
         // the row's Bias, loaded before the wait so its latency overlaps it
         // (keys past S_kv read 0; they are masked below)
@@ -436,10 +438,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32f(tS + lane_off + q * 32, x + q * 32);
         tmem_wait_ld();
-        if constexpr (CAP) {
-#pragma unroll
-          for (int i = 0; i < 128; i += 8) cap_r8(x + i, p.cap_in);
-        }
+        if constexpr (CAP) mx = cap_scores<128>(x, p.cap_in, sl2);
         if constexpr (!RAW) {
 #pragma unroll
           for (int i = 0; i < 128; i += 2) {
@@ -461,6 +460,7 @@ __global__ void __launch_bounds__(384, 1)
         // a tile needs masking where it crosses S_kv or an edge of some row's window
         const Band wb = lds_band(band_slot);
         if ((k0 + C::BN > S_kv) || (k0 + C::BN - 1 > qt0 + wb.hi) || (k0 < qt0 + C::BM - 1 + wb.lo)) {
+          hidden = true;
           const int first = row + wb.lo, last = min(S_kv - 1, row + wb.hi);  // visible keys
 #pragma unroll
           for (int i = 0; i < 128; ++i)
@@ -472,11 +472,10 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < 128; ++i)
           if (k0 + i > lim) x[i] = neg;
       }
-      float mx;
       if (!CAP && (!RAW || sl2 > 0.f)) {
         mx = extreme_of<false, 128>(x);
         if (RAW) mx *= sl2;
-      } else {
+      } else if (!CAP || hidden) {
         mx = extreme_of<true, 128>(x) * sl2;
       }
       // Rescale only when the max grew by more than 8 (a factor 256).

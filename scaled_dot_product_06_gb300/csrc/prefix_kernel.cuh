@@ -358,19 +358,17 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32f(tS + lane_off + q * 32, xs + q * 32);
           tmem_wait_ld();
-          if constexpr (CAP) {
-#pragma unroll
-            for (int e = 0; e < 128; e += 8) cap_r8(xs + e, p.cap_in);
-          }
-          if (k0 + C::BN - 1 > all_see) {
+          float mx = SDPA_NEG_INF;
+          const bool hidden = k0 + C::BN - 1 > all_see;  // the tile has hidden keys
+          if constexpr (CAP) mx = cap_scores<128>(xs, p.cap_in, sl2);
+          if (hidden) {
 #pragma unroll
             for (int e = 0; e < 128; ++e)
               if (k0 + e > last) xs[e] = neg;
           }
-          float mx;
           if (!CAP && sl2 > 0.f)
             mx = extreme_of<false, 128>(xs) * sl2;
-          else
+          else if (!CAP || hidden)
             mx = extreme_of<true, 128>(xs) * sl2;
           // O is rescaled only when the maximum grew by more than 2^8 (fwd_kernel.cuh)
           const bool grow = mx > m + 8.0f;

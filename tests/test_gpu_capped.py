@@ -204,6 +204,39 @@ def test_gradients_against_differences():
         assert abs(got - diff) <= (e * np.abs(d)).sum() + 1e-6, name
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [(-1, 0), (40, 0)])
+def test_not_a_number_stays_where_it_is(d, window):
+    """A key that is not a number reaches the queries that see it, all of them,
+    and no other; a query that is not a number only itself."""
+    x = make_inputs(Shape(1, 2, 300, 300, d, d, 2), "bf16")
+    q, k, v = (x[n].cuda() for n in ("q", "k", "v"))
+    kw = dict(scale=d ** -0.5, window=window, softcap=20.0)
+    o0, lse0 = sdpa_fwd(q, k, v, **kw)
+    bad_k, bad_q = k.clone(), q.clone()
+    bad_k[:, 0, 101] = float("nan")
+    bad_q[:, 1, 77, 3] = float("nan")
+    o, lse = sdpa_fwd(bad_q, bad_k, v, **kw)
+    settled()
+    sees = torch.zeros(2, 300, dtype=torch.bool)
+    sees[0, 101:] = True
+    if window[0] >= 0:
+        sees[0, 101 + window[0] + 1:] = False
+    sees[1, 77] = True
+    sees = sees.cuda()
+    assert torch.isnan(o[0][sees]).all()
+    # Not bit for bit: a visible score shares its reciprocal's roundings with
+    # hidden ones. A score is off by at most cap 2^-20 in each of the two calls,
+    # and so is the log-sum (with its own 2^-20, as in capped_bounds); a P at the
+    # border of a rounding may then round the other way, once in P and in O.
+    cap = 20.0
+    ok = (lse - lse0).abs() <= 2 * (cap + 1 + lse0.abs() + cap) * 2.0 ** -20
+    assert ok[0][~sees].all()
+    u = 2.0 ** -8
+    ok = (o.float() - o0.float()).abs() <= u * (2 * o0.float().abs() + v.float().abs().max()) + 2 * cap * 2.0 ** -20
+    assert ok[0][~sees].all()
+
+
 def test_refusals():
     shp = Shape(1, 2, 64, 64, 64, 64)
     x = make_inputs(shp, "bf16", with_bias=True)
