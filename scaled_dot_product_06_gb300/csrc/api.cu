@@ -799,29 +799,45 @@ sdpa_status_t plan_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64
   const int64_t tiles_p = R <= 128 ? (b + seqs - 1) / seqs : b * per;
   p->row_tiles_p = static_cast<int>(tiles_p);
   p->row_tiles_o = static_cast<int>(per);
-  p->dual_p = tiles_p > 1;
-  p->dual_o = per > 1;
-  const int64_t blocks_p = p->dual_p ? (tiles_p + 1) / 2 : 1, blocks_o = p->dual_o ? (per + 1) / 2 : 1;
+  p->dual_p = tiles_p > 1 && d_qk <= kPrefixDualMax;
+  p->dual_o = per > 1 && d_qk <= kPrefixDualMax;
+  const int64_t blocks_p = p->dual_p ? (tiles_p + 1) / 2 : tiles_p, blocks_o = p->dual_o ? (per + 1) / 2 : per;
   p->row_blocks_p = static_cast<int>(blocks_p);
   p->row_blocks_o = static_cast<int>(blocks_o);
   const int64_t kt_p = (s_prefix + 127) / 128, kt_o = (s_max + 127) / 128;
   const int64_t items_p = blocks_p * h_kv, items_o = blocks_o * b * h_kv;
-  const double visits = static_cast<double>(items_p) * kt_p + static_cast<double>(items_o) * kt_o;
-  const int64_t c = std::max<int64_t>(1, static_cast<int64_t>(std::ceil(visits / (2 * 152))));
-  p->chunk_p = static_cast<int>(std::max<int64_t>(1, std::min(c, kt_p)));
-  p->chunk_o = static_cast<int>(std::max<int64_t>(1, std::min(c, kt_o)));
+  // Key ranges of the items. A CTA's share of the key tiles, the own keys taken
+  // at half of their longest: items of 0.7 of it, but at least 4 tiles of the prefix and
+  // 8 own ones (an item costs about two of either besides), and no more of the
+  // prefix than CTAs; each range of a key set as long as the others. Items are handed out as CTAs ask for them, the
+  // prefix's long ones first. (Dealt out in turn, b64 h32 kv4 d128 behind 16384
+  // keys with own lengths up to 1024 took 47 us.)
+  const double share = (1.1 * static_cast<double>(items_p) * kt_p + 0.5 * static_cast<double>(items_o) * kt_o) / 152;
+  auto cut = [](int64_t kt, double chunk) -> int64_t {  // the key tiles of an item
+    if (kt <= 0) return 1;
+    const int64_t c = std::max<int64_t>(1, std::min(kt, static_cast<int64_t>(chunk)));
+    const int64_t n = (kt + c - 1) / c;
+    return (kt + n - 1) / n;
+  };
+  const double least = std::ceil(static_cast<double>(items_p) * kt_p / 152);
+  p->chunk_p = static_cast<int>(cut(kt_p, std::max({least, std::floor(share * 0.7 / 1.1), 4.0})));
+  p->chunk_o = static_cast<int>(cut(kt_o, std::max(std::ceil(share * 0.7), 8.0)));
   const int64_t sp = (kt_p + p->chunk_p - 1) / p->chunk_p, so = (kt_o + p->chunk_o - 1) / p->chunk_o;
   if (items_p * sp + items_o * so > (int64_t{1} << 30)) return fail(SDPA_ERR_UNSUPPORTED, "too many work items");
   p->splits_p = static_cast<int>(sp);
   p->splits_o = static_cast<int>(so);
   p->items_prefix = static_cast<int>(items_p * sp);
   p->items_own = static_cast<int>(items_o * so);
+  p->grid = static_cast<int>(std::min<int64_t>(152, items_p * sp + items_o * so));
   p->slots_p = static_cast<int>(sp * (p->dual_p ? 1 : 2));
-  p->slots_o = static_cast<int>(so * (p->dual_o ? 1 : 2));
+  p->quart_o = R <= 32;
+  p->slots_o = static_cast<int>(so * (p->dual_o ? 1 : p->quart_o ? 8 : 2));
   p->q_box_p = static_cast<uint32_t>(128 * std::min<int64_t>(R, 128) * seqs);
   p->q_box_o = static_cast<uint32_t>(128 * std::min<int64_t>(R, 128));
-  // partial rows, then their log-sums
-  *bytes = (static_cast<size_t>(p->slots_p + p->slots_o) * rows * (d_v + 1) * sizeof(float) + 255) & ~size_t(255);
+  // partial rows, then their log-sums and the count of items taken
+  *bytes = static_cast<size_t>(p->slots_p + p->slots_o) * ((rows + 7) / 8 * 8 * d_v + rows) * sizeof(float);
+  if (p->items_prefix + p->items_own > p->grid) *bytes += sizeof(int);
+  *bytes = (*bytes + 255) & ~size_t(255);
   return SDPA_OK;
 }
 
@@ -876,13 +892,18 @@ sdpa_status_t sdpa_fwd_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, i
   }
   p.seqlen = seqlen_k;
   p.part = static_cast<float*>(workspace);
-  p.part_lse = p.part + static_cast<int64_t>(p.slots_p + p.slots_o) * p.rows * d_v;
+  p.part_lse = p.part + static_cast<int64_t>(p.slots_p + p.slots_o) * ((p.rows + 7) / 8 * 8) * d_v;
   p.o = o;
   p.lse = lse;
   const bool bf16 = dtype == SDPA_BF16;
   const CUtensorMapDataType tt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (p.items_prefix + p.items_own > 0) {
+    if (p.items_prefix + p.items_own > p.grid) {
+      p.next = reinterpret_cast<int*>(p.part_lse + static_cast<int64_t>(p.slots_p + p.slots_o) * p.rows);
+      const cudaError_t e = launch_prefix_zero(p, st);
+      if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, "item counter launch", e);
+    }
     CUtensorMap m[6] = {};
     const uint32_t box = static_cast<uint32_t>(std::min(p.R, 128));
     if (p.items_prefix > 0) {

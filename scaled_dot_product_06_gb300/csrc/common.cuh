@@ -480,15 +480,18 @@ __device__ __forceinline__ void cap_r8(float* x, float c) {
 // hidden key. One pass for the largest raw score, three values an instruction,
 // shows whether the hold at 30 is needed and whether a score is not a number,
 // and costs less than the holds. Such a score stays one, and alone: hidden
-// keys may hold anything.
+// keys may hold anything. `live`: the row is one (else it has no say in this).
 template <int N>
-__device__ __forceinline__ float cap_scores(float* x, float c, float sl2) {
+__device__ __forceinline__ float cap_scores(float* x, float c, float sl2, bool live = true) {
   const float hi = extreme_of<false, N, true>(x);
-  if (__all_sync(0xffffffffu, c > 0.f && hi * c <= 30.f)) {
+  if (__all_sync(0xffffffffu, !live || (c > 0.f && hi * c <= 30.f))) {
 #pragma unroll
     for (int i = 0; i < N; i += 8) cap_r8<false>(x + i, c);
     return sl2 * rcp(1.f + ex2(hi * c));
   }
+  // the same arithmetic for the rows that would have passed: a row's result
+  // does not depend on the warp's other rows
+  const float top = fminf((c > 0.f ? hi : extreme_of<true, N>(x)) * c, 30.f);
 #pragma unroll
   for (int i = 0; i < N; i += 8) {
     float r[8];
@@ -498,7 +501,7 @@ __device__ __forceinline__ float cap_scores(float* x, float c, float sl2) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[i + e] = x[i + e] == x[i + e] ? r[e] : x[i + e];
   }
-  return sl2 * extreme_of<true, N>(x);
+  return sl2 * rcp(1.f + ex2(top));
 }
 
 template <bool BF16>

@@ -3,7 +3,11 @@
 // over the slots a row has: the prefix's, and as many of the own keys' as its
 // sequence's length fills. A row without a key gets O = 0 and LSE = -inf.
 // Bound by the latency of reading the partials, which the first kernel has
-// just left in L2: WARPS warps share a row's slots where there are many.
+// just left in L2: a warp has 8 rows and 32 columns, whose partials are one line
+// a column group (prefix_part_index), and reads 8 slots of them at once; warps
+// share the slots where there are more. (A warp per row, its slots one after
+// another behind their weights, took 45 us of 38 slots of 2048 rows d128 for
+// 6 us now.)
 #include "common.cuh"
 #include "prefix.cuh"
 
@@ -15,107 +19,130 @@ namespace {
 // call's result does not depend on timing.
 template <bool BF16, int DV, int WARPS>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) {
-  constexpr int ROWS = 8 / WARPS;   // rows a block
-  constexpr int EL = DV / 32;       // elements a lane: 2 or 4
-  __shared__ float s_acc[WARPS > 1 ? 8 : 1][DV];
-  __shared__ float s_ml[WARPS > 1 ? 8 : 1][2];
+  constexpr int UNITS = 8 / WARPS;  // slabs' column parts a block
+  __shared__ float4 s_acc[WARPS > 1 ? 8 : 1][64];
+  __shared__ float s_ml[WARPS > 1 ? 8 : 1][8][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + warp / WARPS;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * UNITS + warp / WARPS;
   const int w = warp % WARPS;
+  constexpr int PARTS = DV / 32;
+  const int64_t row = unit / PARTS * 8 + (lane & 7);    // this lane's row
+  const int c0 = static_cast<int>(unit % PARTS) * 8 + (lane >> 3);  // its column groups: c0, c0 + 4
   const bool live = row < p.rows;
-  int n = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
+  int n = 0;  // slots of the row
   if (live) {
     n = p.slots_p;
     if (p.slots_o > 0) {
       const int b = static_cast<int>(row / (static_cast<int64_t>(p.H_kv) * p.R));
       const int keys = min(max(__ldg(p.seqlen + b), 0), p.s_max);
-      n += ((keys + 127) / 128 + p.chunk_o - 1) / p.chunk_o * (p.dual_o ? 1 : 2);
+      const int tiles = (keys + 127) / 128, chunks = (tiles + p.chunk_o - 1) / p.chunk_o;
+      n += chunks * (p.dual_o ? 1 : p.quart_o ? 8 : 2);
+      // an item of one key tile: warpgroup 1 has none, nor have warps behind the last key
+      if (!p.dual_o && chunks > 0 && tiles - (chunks - 1) * p.chunk_o == 1)
+        n -= p.quart_o ? 8 - ((keys - 1) % 128 / 32 + 1) : 1;
     }
   }
-  float m = SDPA_NEG_INF, l = 0.f, acc[EL];
+  int most = n;  // of the slab's rows
 #pragma unroll
-  for (int e = 0; e < EL; ++e) acc[e] = 0.f;
-  // 32 slots at a time, one L a lane: their weights are known before the rows
-  // are read, so the reads do not wait for one another
-  for (int s0 = w * 32; s0 < n; s0 += WARPS * 32) {
-    const int cnt = min(32, n - s0);
-    const float L = lane < cnt ? p.part_lse[(s0 + lane) * p.rows + row] : SDPA_NEG_INF;
-    float mx = L;
+  for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  float m = SDPA_NEG_INF, l = 0.f;
+  float4 a0 = make_float4(0.f, 0.f, 0.f, 0.f), a1 = a0;
+  const float4* part = reinterpret_cast<const float4*>(p.part) + c0 * 8;
+  for (int s0 = w * 8; s0 < most; s0 += WARPS * 8) {
+    // 8 slots, all read before their weights are known, and left out where the
+    // row has none (what was not written may be NaN)
+    float4 v0[8], v1[8];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(m, mx);
-    if (mn == SDPA_NEG_INF) continue;
-    const float keep = ex2(m - mn), wt = ex2(L - mn);
+    for (int i = 0; i < 8; ++i) {
+      const float4* at = part + prefix_part_index(min(s0 + i, most - 1), p.rows, min(row, p.rows - 1), DV);
+      v0[i] = __ldcg(at);
+      v1[i] = __ldcg(at + 32);
+    }
+    // lane: slots s0 + (lane >> 3) and 4 further of its row
+    const int i0 = s0 + (lane >> 3), i1 = i0 + 4;
+    const float L0 = i0 < n ? __ldcg(p.part_lse + i0 * p.rows + row) : SDPA_NEG_INF;
+    const float L1 = i1 < n ? __ldcg(p.part_lse + i1 * p.rows + row) : SDPA_NEG_INF;
+    float mx = fmaxf(L0, L1);
+#pragma unroll
+    for (int o = 16; o > 4; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(m, mx), base = mn == SDPA_NEG_INF ? 0.f : mn;
+    const float keep = ex2(m - base), w0 = ex2(L0 - base), w1 = ex2(L1 - base);
     m = mn;
-    float sum = wt;
+    l *= keep;
+    a0.x *= keep, a0.y *= keep, a0.z *= keep, a0.w *= keep;
+    a1.x *= keep, a1.y *= keep, a1.z *= keep, a1.w *= keep;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = fmaf(l, keep, sum);
-#pragma unroll
-    for (int e = 0; e < EL; ++e) acc[e] *= keep;
-    const float* src = p.part + (s0 * p.rows + row) * DV + lane * EL;
-#pragma unroll 8
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, wt, i);
-      const bool some = __shfl_sync(0xffffffffu, L, i) != SDPA_NEG_INF;  // else its O was not written
-      float v[EL];
-#pragma unroll
-      for (int e = 0; e < EL; ++e) v[e] = 0.f;
-      if (some) {
-        if constexpr (EL == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(src + i * p.rows * DV);
-          v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-        } else {
-          const float2 f = *reinterpret_cast<const float2*>(src + i * p.rows * DV);
-          v[0] = f.x, v[1] = f.y;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < EL; ++e) acc[e] = fmaf(wi, v[e], acc[e]);
+    for (int i = 0; i < 8; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, i < 4 ? w0 : w1, (i & 3) * 8 + (lane & 7));
+      l += wi;
+      const bool some = wi > 0.f;
+      a0.x = fmaf(wi, some ? v0[i].x : 0.f, a0.x), a0.y = fmaf(wi, some ? v0[i].y : 0.f, a0.y);
+      a0.z = fmaf(wi, some ? v0[i].z : 0.f, a0.z), a0.w = fmaf(wi, some ? v0[i].w : 0.f, a0.w);
+      a1.x = fmaf(wi, some ? v1[i].x : 0.f, a1.x), a1.y = fmaf(wi, some ? v1[i].y : 0.f, a1.y);
+      a1.z = fmaf(wi, some ? v1[i].z : 0.f, a1.z), a1.w = fmaf(wi, some ? v1[i].w : 0.f, a1.w);
     }
   }
   if constexpr (WARPS > 1) {
-#pragma unroll
-    for (int e = 0; e < EL; ++e) s_acc[warp][lane * EL + e] = acc[e];
-    if (lane == 0) {
-      s_ml[warp][0] = m;
-      s_ml[warp][1] = l;
+    s_acc[warp][lane] = a0;
+    s_acc[warp][lane + 32] = a1;
+    if (lane < 8) {
+      s_ml[warp][lane][0] = m;
+      s_ml[warp][lane][1] = l;
     }
     __syncthreads();
     if (w != 0) return;
     for (int i = 1; i < WARPS; ++i) {
-      const float mo = s_ml[warp + i][0], lo = s_ml[warp + i][1];
-      if (mo == SDPA_NEG_INF) continue;
-      const float mn = fmaxf(m, mo);
-      const float keep = ex2(m - mn), add = ex2(mo - mn);
+      const float mo = s_ml[warp + i][lane & 7][0], lo = s_ml[warp + i][lane & 7][1];
+      const float mn = fmaxf(m, mo), base = mn == SDPA_NEG_INF ? 0.f : mn;
+      const float keep = ex2(m - base), add = ex2(mo - base);
       m = mn;
       l = fmaf(l, keep, lo * add);
-#pragma unroll
-      for (int e = 0; e < EL; ++e) acc[e] = fmaf(acc[e], keep, add * s_acc[warp + i][lane * EL + e]);
+      const float4 b0 = s_acc[warp + i][lane], b1 = s_acc[warp + i][lane + 32];
+      a0.x = fmaf(a0.x, keep, add * b0.x), a0.y = fmaf(a0.y, keep, add * b0.y);
+      a0.z = fmaf(a0.z, keep, add * b0.z), a0.w = fmaf(a0.w, keep, add * b0.w);
+      a1.x = fmaf(a1.x, keep, add * b1.x), a1.y = fmaf(a1.y, keep, add * b1.y);
+      a1.z = fmaf(a1.z, keep, add * b1.z), a1.w = fmaf(a1.w, keep, add * b1.w);
     }
   }
   if (!live) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint8_t* dst = static_cast<uint8_t*>(p.o) + (row * DV + lane * EL) * 2;
-  if constexpr (EL == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv),
-                                                pack2<BF16>(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : SDPA_NEG_INF;
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + row * DV * 2);
+  dst[c0] = make_uint2(pack2<BF16>(a0.x * inv, a0.y * inv), pack2<BF16>(a0.z * inv, a0.w * inv));
+  dst[c0 + 4] = make_uint2(pack2<BF16>(a1.x * inv, a1.y * inv), pack2<BF16>(a1.z * inv, a1.w * inv));
+  if (c0 == 0) p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : SDPA_NEG_INF;
 }
 
 template <bool BF16, int DV>
 cudaError_t launch_join_d(const PrefixParams& p, cudaStream_t st) {
-  // one warp reads 32 slots at a time
-  if (p.slots_p + p.slots_o > 32)
-    prefix_join_kernel<BF16, DV, 8><<<static_cast<unsigned>(p.rows), 256, 0, st>>>(p);
-  else
-    prefix_join_kernel<BF16, DV, 1><<<static_cast<unsigned>((p.rows + 7) / 8), 256, 0, st>>>(p);
-  return cudaGetLastError();
+  // a warp reads 8 slots at a time; more than that are shared by up to 8 warps
+  const int n = p.slots_p + p.slots_o;
+  const int warps = n <= 8 ? 1 : n <= 16 ? 2 : n <= 32 ? 4 : 8;
+  auto kern = warps == 1   ? prefix_join_kernel<BF16, DV, 1>
+              : warps == 2 ? prefix_join_kernel<BF16, DV, 2>
+              : warps == 4 ? prefix_join_kernel<BF16, DV, 4>
+                           : prefix_join_kernel<BF16, DV, 8>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(((p.rows + 7) / 8 * (DV / 32) * warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  // the launch itself overlaps the end of the kernel that leaves the partials
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = p.items_prefix + p.items_own > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+__global__ void prefix_zero_kernel(int* n) { *n = 0; }
+
 }  // namespace
+
+cudaError_t launch_prefix_zero(const PrefixParams& p, cudaStream_t st) {
+  prefix_zero_kernel<<<1, 1, 0, st>>>(p.next);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_prefix_join(bool bf16, int d_v, const PrefixParams& p, cudaStream_t st) {
   if (d_v == 64) return bf16 ? launch_join_d<true, 64>(p, st) : launch_join_d<false, 64>(p, st);

@@ -11,22 +11,40 @@
 // and values are read once for the batch and the products fill tcgen05 tiles;
 // the own keys are a stream of their own per sequence. Both are cut along the
 // keys into work items; an item leaves normalised fp32 rows O_s and their
-// log2-sum-exps L_s, and a second kernel joins them:
+// log2-sum-exps L_s, and a second kernel joins them (prefix_join.cu):
 //   L = log2 sum_s 2^L_s,   O = sum_s 2^(L_s - L) O_s.
+// Items are handed out as CTAs ask for them, since the lengths are known on the
+// device only: the producer takes a number from a counter, one ahead, and
+// tells it to the other roles through a ring in shared memory. Which CTA has an
+// item does not change its result.
+//
+// Measured (b64 h32 kv4 d128 bf16 behind 16384 keys, own lengths up to 1024):
+// 36 us, and 7 us the join, for 14 us of bytes and 9 us of products: the start
+// (5 us), filling and emptying the pipeline at each item's ends (about 2 us) and
+// the items' grain are the rest. Own keys alone, 152 sequences of 4096: 5.7 TB/s;
+// a prefix of 131072 for 512 rows a K/V head: 1.4 PFLOP/s. Equal runs of visits
+// for each CTA instead of items (a stream cut at any tile, more partials, every
+// row block's borders found by a scan of the lengths) took 51 us there.
 //
 // One persistent CTA an SM, two softmax warpgroups, one MMA issuer, one TMA
 // producer, as in the forward (fwd_kernel.cuh). An item runs in one of two
 // ways:
-//   dual    (more than 128 rows) warpgroup t has the rows of tile t; both tiles
+//   dual    (more than 128 rows, d_qk up to 128) warpgroup t has the rows of tile t; both tiles
 //           meet every key tile, which is loaded once for them;
 //   single  (up to 128 rows: a decoding step's own keys, where the K/V stream
 //           from memory is the limit) both warpgroups have the same rows and take
 //           the item's key tiles in turns, each with its own running maximum,
 //           sum and O in tensor memory, and each leaves a partial of its own;
-//           one's softmax hides behind the other's products.
+//           one's softmax hides behind the other's products. Own keys of up to
+//           32 rows go a step further (quart): Q lies four times in its tile, once
+//           for each warp's lanes, and a warp takes a quarter of a tile's keys, P
+//           of the others being 0: a warp alone with 128 columns of 8 rows would
+//           be what the stream waits for. Each warp leaves a partial.
 // MMA order per round: O_0 += P_0 V, S_0 of the next round, then the same for
 // warpgroup 1.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "prefix.cuh"
 
@@ -38,14 +56,16 @@ struct PrefixCfg {
   static constexpr int Q_BYTES = BM * DQK * 2;
   static constexpr int K_BYTES = BN * DQK * 2;
   static constexpr int V_BYTES = BN * DV * 2;
-  static constexpr int AVAIL = 227 * 1024 - 2 * Q_BYTES - 256 - 1024;
+  static constexpr int BAR_BYTES = 384;
+  static constexpr int Q_TILES = DQK <= kPrefixDualMax ? 2 : 1;
+  static constexpr int AVAIL = 227 * 1024 - Q_TILES * Q_BYTES - BAR_BYTES - 1024;
   static constexpr int FIT = AVAIL / (K_BYTES + V_BYTES);
   static constexpr int STAGES = FIT >= 4 ? 4 : FIT;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_K = OFF_Q + Q_TILES * Q_BYTES;
   static constexpr int OFF_V = OFF_K + STAGES * K_BYTES;
   static constexpr int OFF_BAR = OFF_V + STAGES * V_BYTES;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;
   static constexpr int THREADS = 384;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t T_S = 0, T_O = 256;
@@ -55,9 +75,11 @@ struct PrefixCfg {
 };
 
 // Barriers: Q full and free, S / P / O per warpgroup, V landed (for the
-// warpgroup that clears its rows behind the last key), rings of K and V.
+// warpgroup that clears its rows behind the last key), rings of K and V, ring
+// of item numbers.
 enum : int { PB_Q = 0, PB_QE, PB_S, PB_P = PB_S + 2, PB_O = PB_P + 2, PB_VZ = PB_O + 2, PB_DRAIN = PB_VZ + 2, PB_KF,
-             PB_KE = PB_KF + 4, PB_VF = PB_KE + 4, PB_VE = PB_VF + 4, PB_COUNT = PB_VE + 4 };
+             PB_KE = PB_KF + 4, PB_VF = PB_KE + 4, PB_VE = PB_VF + 4,
+             PB_I = PB_VE + 4, PB_IE = PB_I + 4, PB_COUNT = PB_IE + 4 };
 
 // One work item, decoded alike by every role.
 struct PrefixItem {
@@ -66,6 +88,7 @@ struct PrefixItem {
   int tile;     // first row tile
   bool has1;    // dual: the second row tile exists
   bool dual;
+  bool quart;   // rows repeated for each warp's lanes, which take a quarter of the keys
   int k0, n;    // first key tile, key tiles (0: nothing to do)
   int keys;     // keys of the source
   int slot;     // partial slot of warpgroup 0 (single: warpgroup 1 has the next)
@@ -87,6 +110,7 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixParams& p, int idx
     it.keys = p.s_prefix;
     it.k0 = sp * p.chunk_p;
     it.n = min(p.chunk_p, (it.keys + 127) / 128 - it.k0);
+    it.quart = false;
     it.slot = it.dual ? sp : 2 * sp;
   } else {
     idx -= p.items_prefix;
@@ -102,7 +126,8 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixParams& p, int idx
     it.keys = min(max(__ldg(p.seqlen + it.b), 0), p.s_max);
     it.k0 = sp * p.chunk_o;
     it.n = max(0, min(p.chunk_o, (it.keys + 127) / 128 - it.k0));
-    it.slot = p.slots_p + (it.dual ? sp : 2 * sp);
+    it.quart = p.quart_o != 0;
+    it.slot = p.slots_p + (it.dual ? sp : it.quart ? 8 * sp : 2 * sp);
   }
   return it;
 }
@@ -137,12 +162,14 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + PB_COUNT);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  static_assert((PB_COUNT + 1) * 8 <= 256, "barrier region");
+  volatile int* items = reinterpret_cast<volatile int*>(tmem_slot + 2);  // ring of 4
+  static_assert((PB_COUNT + 3) * 8 <= C::BAR_BYTES, "barrier region");
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < PB_COUNT; ++i) mbar_init(bar(i), (i == PB_P || i == PB_P + 1) ? 128u : 1u);
+    // (a number is read by the MMA issuer and the eight softmax warps)
+    for (int i = 0; i < PB_COUNT; ++i) mbar_init(bar(i), (i == PB_P || i == PB_P + 1) ? 128u : i >= PB_IE ? 9u : 1u);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -156,6 +183,19 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tbase = *tmem_slot;
   const ErrCtx ec{p.err, abort_flag};
   const int n_items = p.items_prefix + p.items_own;
+  // The `u`-th item of this CTA (n_items: no more). Where there are more items
+  // than CTAs the producer tells it; else each has one (which may be empty).
+  auto next_item = [&](int u, int* idx) -> bool {
+    if (p.next == nullptr) {
+      *idx = u == 0 ? static_cast<int>(blockIdx.x) : n_items;
+      return true;
+    }
+    if (!mbar_wait(bar(PB_I + (u & 3)), (u >> 2) & 1, ec, kSiteFwdSoftmax)) return false;
+    *idx = items[u & 3];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(PB_IE + (u & 3)));
+    return true;
+  };
 
   if (warp >= 8) {
     setmaxnreg_dec<C::REG_OTHER>();
@@ -164,32 +204,26 @@ __global__ void __launch_bounds__(384, 1)
       int nq = 0;          // items loaded
       int nk = 0, nv = 0;  // key tiles loaded
       bool ok = true;
-      for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
-        const PrefixItem it = prefix_item(p, idx);
-        if (it.n == 0) continue;
-        if (!(ok = mbar_wait(bar(PB_QE), (nq & 1) ^ 1, ec, kSiteFwdLoad, true, true))) break;
-        if (lane == 0) {
-          const CUtensorMap* mq = it.own ? &tmQo : &tmQp;
-          const uint32_t box = it.own ? p.q_box_o : p.q_box_p;  // bytes a 64-column box
-          mbar_arrive_expect_tx(bar(PB_Q), (it.has1 ? 2 : 1) * (DQK / 64) * box);
-#pragma unroll 1
-          for (int t = 0; t < (it.has1 ? 2 : 1); ++t) {
-            // rows of row tile `tile`: whole sequences' R rows each (R <= 128), else
-            // 128 rows of one sequence
-            int x0, b0;
-            if (p.R <= 128) {
-              x0 = 0;
-              b0 = it.own ? it.b : (it.tile + t) * p.seqs_tile;
-            } else {
-              const int per = (p.R + 127) / 128;
-              b0 = it.own ? it.b : (it.tile + t) / per;
-              x0 = (it.own ? it.tile + t : (it.tile + t) % per) * 128;
-            }
-            for (int c = 0; c < DQK / 64; ++c)
-              tma_load_4d(sQ + t * C::Q_BYTES + c * C::BM * 128, mq, bar(PB_Q), c * 64, x0, b0, it.hk);
+      int idx = blockIdx.x, ahead = 0;
+      // (launched while the kernel that clears the counter runs)
+      if (p.next != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (;; idx = __shfl_sync(0xffffffffu, ahead, 0)) {
+        // the number after this one, asked for now and looked at afterwards
+        ahead = n_items;
+        if (lane == 0 && idx < n_items && p.next != nullptr)
+          ahead = static_cast<int>(gridDim.x) + atomicAdd(p.next, 1);
+        PrefixItem it;
+        if (idx < n_items) it = prefix_item(p, idx);
+        if (idx < n_items && it.n == 0) continue;
+        if (p.next != nullptr) {
+          if (!(ok = mbar_wait(bar(PB_IE + (nq & 3)), ((nq >> 2) & 1) ^ 1, ec, kSiteFwdLoad, true, true))) break;
+          if (lane == 0) {
+            items[nq & 3] = idx;
+            mbar_arrive(bar(PB_I + (nq & 3)));
           }
+          __syncwarp();
         }
-        ++nq;
+        if (idx >= n_items) break;
         const CUtensorMap* mk = it.own ? &tmKo : &tmKp;
         const CUtensorMap* mv = it.own ? &tmVo : &tmVp;
         const int z = it.own ? it.b * p.H_kv + it.hk : it.hk;
@@ -205,6 +239,37 @@ __global__ void __launch_bounds__(384, 1)
               tma_load_3d(sK + s * C::K_BYTES + c * C::BN * 128, mk, bar(PB_KF + s), c * 64, row, z);
           }
           ++nk;
+          if (j == 0) {  // the item's Q, behind its first keys: they need not wait for Q's buffer
+            if (!(ok = mbar_wait(bar(PB_QE), (nq & 1) ^ 1, ec, kSiteFwdLoad, true, true))) break;
+            if (lane == 0) {
+              const CUtensorMap* mq = it.own ? &tmQo : &tmQp;
+              const uint32_t box = it.own ? p.q_box_o : p.q_box_p;  // bytes a 64-column box
+              mbar_arrive_expect_tx(bar(PB_Q), (it.has1 ? 2 : it.quart ? 4 : 1) * (DQK / 64) * box);
+              if (it.quart) {
+#pragma unroll 1
+                for (int w = 1; w < 4; ++w)
+                  for (int c = 0; c < DQK / 64; ++c)
+                    tma_load_4d(sQ + c * C::BM * 128 + w * 32 * 128, mq, bar(PB_Q), c * 64, 0, it.b, it.hk);
+              }
+#pragma unroll 1
+              for (int t = 0; t < (it.has1 ? 2 : 1); ++t) {
+                // rows of row tile `tile`: whole sequences' R rows each (R <= 128), else
+                // 128 rows of one sequence
+                int x0, b0;
+                if (p.R <= 128) {
+                  x0 = 0;
+                  b0 = it.own ? it.b : (it.tile + t) * p.seqs_tile;
+                } else {
+                  const int per = (p.R + 127) / 128;
+                  b0 = it.own ? it.b : (it.tile + t) / per;
+                  x0 = (it.own ? it.tile + t : (it.tile + t) % per) * 128;
+                }
+                for (int c = 0; c < DQK / 64; ++c)
+                  tma_load_4d(sQ + t * C::Q_BYTES + c * C::BM * 128, mq, bar(PB_Q), c * 64, x0, b0, it.hk);
+              }
+            }
+            ++nq;
+          }
           if (!(ok = mbar_wait(bar(PB_VE + s), ph ^ 1, ec, kSiteFwdLoad, true, true))) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(bar(PB_VF + s), C::V_BYTES);
@@ -214,6 +279,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           ++nv;
         }
+        if (!ok) break;
       }
       __syncwarp();
       // Every copy issued must land before the CTA can retire; on the healthy
@@ -235,9 +301,9 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t pph[2] = {0u, 0u};  // P phases consumed
       int nq = 0, base = 0;        // items, key tiles before this item
       bool ok = true;
-      for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+      for (int idx; (ok = next_item(nq, &idx)) && idx < n_items;) {
         const PrefixItem it = prefix_item(p, idx);
-        if (it.n == 0) continue;
+        if (it.n == 0) break;
         auto issue_s = [&](int t, int i) -> bool {  // S_t = Q K^T of its round i
           const int j = prefix_tile(it, t, i), g = base + j;
           if (!mbar_wait_w(bar(PB_KF + g % ST), (g / ST) & 1, ec, kSiteFwdMma)) return false;
@@ -290,6 +356,7 @@ __global__ void __launch_bounds__(384, 1)
               umma_commit_w(bar(PB_O + t));
           }
         }
+        if (!ok) break;
         ++nq;
         base += it.n;
       }
@@ -307,18 +374,18 @@ __global__ void __launch_bounds__(384, 1)
     const uint64_t sl22 = f2(sl2, sl2);
     const float neg = (CAP || sl2 < 0.f) ? -SDPA_NEG_INF : SDPA_NEG_INF;  // masked raw score
     uint32_t sph = 0, oph = 0, zph = 0;  // S, O and V-landed phases
-    int base = 0;
+    int base = 0, ni = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+    for (int idx; (ok = next_item(ni, &idx)) && idx < n_items; ++ni) {
       const PrefixItem it = prefix_item(p, idx);
-      if (it.n == 0) continue;
+      if (it.n == 0) break;
       // this thread's row: sequence b, row x of its R
       const int tile = it.tile + (it.dual ? t : 0);
       int b, x;
       bool row_ok;
       if (p.R <= 128) {
-        const int off = li / p.R;
-        x = li - off * p.R;
+        const int off = (it.quart ? lane : li) / p.R;
+        x = (it.quart ? lane : li) - off * p.R;
         b = it.own ? it.b : tile * p.seqs_tile + off;
         row_ok = it.own ? off == 0 : (off < p.seqs_tile && b < p.B);
       } else {
@@ -333,6 +400,78 @@ __global__ void __launch_bounds__(384, 1)
       const int last = it.own ? it.keys - p.s_q + x % p.s_q : it.keys - 1;
       const int all_see = it.own ? it.keys - p.s_q : it.keys - 1;  // visible to every row
       float m = SDPA_NEG_INF, l = 0.f;
+      // columns col .. col + N - 1 of the tile, whose first is key k0 + col; P of the
+      // others is 0
+      auto softmax = [&](auto width, int col, int k0, bool rescale) {
+        constexpr int N = decltype(width)::value;
+        k0 += col;
+        float xs[N];
+#pragma unroll
+        for (int q = 0; q < N / 32; ++q) tmem_ld32f(tS + lane_off + col + q * 32, xs + q * 32);
+        tmem_wait_ld();
+        float mx = SDPA_NEG_INF;
+        const bool hidden = k0 + N - 1 > all_see;  // there are hidden keys
+        if constexpr (CAP) mx = cap_scores<N>(xs, p.cap_in, sl2, row_ok);
+        if (hidden) {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (k0 + e > last) xs[e] = neg;
+        }
+        if (!CAP && sl2 > 0.f)
+          mx = extreme_of<false, N>(xs) * sl2;
+        else if (!CAP || hidden)
+          mx = extreme_of<true, N>(xs) * sl2;
+        // O is rescaled only when the maximum grew by more than 2^8 (fwd_kernel.cuh)
+        const bool grow = mx > m + 8.0f;
+        float alpha = 1.0f;
+        if (grow) {
+          alpha = ex2(m - mx);
+          m = mx;
+        }
+        if (rescale && __any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int q = 0; q < DV / 16; ++q) {
+            uint32_t rr[16];
+            tmem_ld16(tO + lane_off + q * 16, rr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
+            tmem_st16(tO + lane_off + q * 16, rr);
+          }
+        }
+        l *= alpha;
+        const float mu = (m == SDPA_NEG_INF) ? 0.f : m;
+        const uint64_t nm2 = f2(-mu, -mu);
+        uint64_t sa = f2(0.f, 0.f), sb = f2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+          const float2 a = f2split(fma2(f2(xs[e], xs[e + 1]), sl22, nm2));
+          const float2 c = f2split(fma2(f2(xs[e + 2], xs[e + 3]), sl22, nm2));
+          xs[e] = ex2(a.x);
+          xs[e + 1] = ex2(a.y);
+          xs[e + 2] = ex2(c.x);
+          xs[e + 3] = ex2(c.y);
+          sa = add2(sa, f2(xs[e], xs[e + 1]));
+          sb = add2(sb, f2(xs[e + 2], xs[e + 3]));
+        }
+        const float2 u = f2split(sa), w = f2split(sb);
+        l += (u.x + u.y) + (w.x + w.y);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pk[e] = N == 128 ? pack2<BF16>(xs[(q * 32 + 2 * e) % N], xs[(q * 32 + 2 * e + 1) % N]) : 0u;
+          if (N == 128 || q * 32 != col) tmem_st16(tS + lane_off + q * 16, pk);
+        }
+        if constexpr (N == 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(xs[2 * e], xs[2 * e + 1]);
+          tmem_st16(tS + lane_off + col / 2, pk);
+        }
+        tmem_wait_st();
+      };
       int i = 0;
       for (; ok && prefix_has(it, t, i); ++i) {
         const int j = prefix_tile(it, t, i);
@@ -354,65 +493,10 @@ __global__ void __launch_bounds__(384, 1)
         sph ^= 1u;
         tc_fence_after();
         if (warp_ok) {
-          float xs[128];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32f(tS + lane_off + q * 32, xs + q * 32);
-          tmem_wait_ld();
-          float mx = SDPA_NEG_INF;
-          const bool hidden = k0 + C::BN - 1 > all_see;  // the tile has hidden keys
-          if constexpr (CAP) mx = cap_scores<128>(xs, p.cap_in, sl2);
-          if (hidden) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (k0 + e > last) xs[e] = neg;
-          }
-          if (!CAP && sl2 > 0.f)
-            mx = extreme_of<false, 128>(xs) * sl2;
-          else if (!CAP || hidden)
-            mx = extreme_of<true, 128>(xs) * sl2;
-          // O is rescaled only when the maximum grew by more than 2^8 (fwd_kernel.cuh)
-          const bool grow = mx > m + 8.0f;
-          float alpha = 1.0f;
-          if (grow) {
-            alpha = ex2(m - mx);
-            m = mx;
-          }
-          if (i > 0 && __any_sync(0xffffffffu, grow)) {
-#pragma unroll
-            for (int q = 0; q < DV / 16; ++q) {
-              uint32_t rr[16];
-              tmem_ld16(tO + lane_off + q * 16, rr);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
-              tmem_st16(tO + lane_off + q * 16, rr);
-            }
-          }
-          l *= alpha;
-          const float mu = (m == SDPA_NEG_INF) ? 0.f : m;
-          const uint64_t nm2 = f2(-mu, -mu);
-          uint64_t sa = f2(0.f, 0.f), sb = f2(0.f, 0.f);
-#pragma unroll
-          for (int e = 0; e < 128; e += 4) {
-            const float2 a = f2split(fma2(f2(xs[e], xs[e + 1]), sl22, nm2));
-            const float2 c = f2split(fma2(f2(xs[e + 2], xs[e + 3]), sl22, nm2));
-            xs[e] = ex2(a.x);
-            xs[e + 1] = ex2(a.y);
-            xs[e + 2] = ex2(c.x);
-            xs[e + 3] = ex2(c.y);
-            sa = add2(sa, f2(xs[e], xs[e + 1]));
-            sb = add2(sb, f2(xs[e + 2], xs[e + 3]));
-          }
-          const float2 u = f2split(sa), w = f2split(sb);
-          l += (u.x + u.y) + (w.x + w.y);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(xs[q * 32 + 2 * e], xs[q * 32 + 2 * e + 1]);
-            tmem_st16(tS + lane_off + q * 16, pk);
-          }
-          tmem_wait_st();
+          if (it.quart)
+            softmax(std::integral_constant<int, 32>{}, (warp & 3) * 32, k0, i > 0);
+          else
+            softmax(std::integral_constant<int, 128>{}, 0, k0, i > 0);
         }
         tc_fence_before();
         mbar_arrive(bar(PB_P + t));
@@ -427,11 +511,11 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
       }
       const int64_t ri = (static_cast<int64_t>(row_ok ? b : 0) * p.H_kv + it.hk) * p.R + (row_ok ? x : 0);
-      const int slot = it.slot + (it.dual ? 0 : t);
+      const int slot = it.slot + (it.dual ? 0 : it.quart ? 4 * t + (warp & 3) : t);
       const int64_t at = slot * p.rows + ri;
       if (i > 0 && warp_ok) {
         const float inv = l > 0.f ? 1.0f / l : 0.f;
-        float4* dst = reinterpret_cast<float4*>(p.part + at * DV);
+        float4* dst = reinterpret_cast<float4*>(p.part) + prefix_part_index(slot, p.rows, ri, DV);
 #pragma unroll
         for (int q = 0; q < DV / 32; ++q) {
           uint32_t rr[32];
@@ -440,7 +524,7 @@ __global__ void __launch_bounds__(384, 1)
           if (row_ok && l > 0.f) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[q * 8 + e] = make_float4(__uint_as_float(rr[4 * e]) * inv, __uint_as_float(rr[4 * e + 1]) * inv,
+              dst[(q * 8 + e) * 8] = make_float4(__uint_as_float(rr[4 * e]) * inv, __uint_as_float(rr[4 * e + 1]) * inv,
                                            __uint_as_float(rr[4 * e + 2]) * inv,
                                            __uint_as_float(rr[4 * e + 3]) * inv);
           }
@@ -466,9 +550,18 @@ cudaError_t launch_prefix_t(const CUtensorMap (&m)[6], const PrefixParams& p, cu
                                                      : sdpa_prefix_kernel<DQK, DV, BF16, false>;
   cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, C::REG_LAUNCH);
   if (e != cudaSuccess) return e;
-  const int items = p.items_prefix + p.items_own;
-  kern<<<items < 152 ? items : 152, C::THREADS, C::SMEM, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  // the launch overlaps the kernel that clears the counter
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = p.next != nullptr ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], p);
 }
 
 }  // namespace sdpa

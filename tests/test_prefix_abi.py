@@ -38,8 +38,8 @@ def test_refusals(lib):  # noqa: F811
 def test_workspace_size(lib):  # noqa: F811
     size = lib.sdpa_fwd_prefix_workspace_size
     assert size(2, 4, 2, 1, 0, 0, 64, 64) == 0  # no key at all
-    # one key tile each: two slots of the prefix and two of the own keys, 8 rows
-    assert size(2, 4, 2, 1, 100, 50, 64, 64) == (4 * 8 * 65 * 4 + 255) // 256 * 256
+    # one key tile each: two slots of the prefix and eight of the own keys, 8 rows
+    assert size(2, 4, 2, 1, 100, 50, 64, 64) == (10 * 8 * 65 * 4 + 255) // 256 * 256
     assert size(2, 4, 3, 1, 100, 50, 64, 64) == 0
     assert size(2, 4, 2, 1, 100, 50, 96, 96) == 0
 
