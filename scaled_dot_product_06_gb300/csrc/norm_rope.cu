@@ -17,8 +17,11 @@
 // copies, each thread its own 16 bytes and reading back only those (no
 // barrier), so the loads in flight hold no registers: with plain loads, four
 // rows a thread ahead of their use, a call at b1 s16384 h32 + 2 x 4, d = 128
-// took 74 us (68% of the copy rate) and its backward at b4 s2048, 3 x 16
-// heads, 113 us (36%).
+// took 74 us (68% of the copy rate; now 59 us, 85%) and its backward at b4
+// s2048, 3 x 16 heads, 113 us (36%; now 65 us, 62%: its reads are 512-byte
+// pieces, two arrays at once, and a warp waits for three rounds of shuffles a
+// row). Shorter walks than 16 heads lose more to the angles than they gain in
+// grain: 65 us at 8, 72 us at 4, for 60 us of the kernel alone.
 #include <algorithm>
 
 #include "common.cuh"
@@ -378,6 +381,7 @@ __global__ void __launch_bounds__(1024) dw_reduce_kernel(const float* __restrict
   const bool keys = blockIdx.y != 0;
   void* dw = keys ? dw_k : dw_q;
   if (dw == nullptr) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial rows are written
   float s = 0.f;
   for (int i = (keys ? k0 : q0) + r; i < (keys ? k1 : k0); i += 32) s += part[static_cast<int64_t>(i) * d + col];
   sum[r][c] = s;
@@ -424,21 +428,25 @@ int norm_rope_plan(NormRopeParams* p, bool backward) {
   };
   p->seg = 16;
   while (p->seg > 1 && warps(p->seg) < 32 * 152) p->seg /= 2;
-  int64_t need[3] = {0, 0, 0}, rows = 0;
+  // the time of a kind's rows: with a norm backward 3 rows move and the sums
+  // are taken, else 2 rows move
+  auto cost = [&](int i) -> int64_t { return p->kind[i].heads * (p->kind[i].weight != nullptr ? 4 : 2); };
+  int64_t need[3] = {0, 0, 0}, all = 0;
   for (int i = 0; i < p->n_kinds; ++i) {
     const int64_t units = n_tb * ((p->kind[i].heads + p->seg - 1) / p->seg);
     if (units >= (int64_t{1} << 31)) return -1;
     p->kind[i].units = static_cast<uint32_t>(units);
     need[i] = (units + W - 1) / W;
-    rows += p->kind[i].heads;
+    all += cost(i);
   }
   // the backward's blocks loop, each leaving one partial row of dw: the three
-  // resident an SM, shared among the kinds by their rows
+  // resident an SM, shared among the kinds by their time (by their rows, b4 s2048
+  // of 3 x 16 heads d128 took 67 us for 60: the values' blocks ended early)
   const int64_t most = 3 * 152;
   int64_t at = 0;
   for (int i = 0; i < p->n_kinds; ++i) {
     p->kind[i].block0 = static_cast<int>(at);
-    const int64_t share = std::max<int64_t>(1, (most * p->kind[i].heads + rows / 2) / rows);
+    const int64_t share = std::max<int64_t>(1, (most * cost(i) + all / 2) / all);
     at += backward ? std::min(need[i], share) : need[i];
     if (at > 0x7fffffff) return -1;
   }
@@ -466,9 +474,18 @@ cudaError_t launch_norm_rope_bwd(bool bf16, const NormRopeParams& p, int blocks,
   if (e != cudaSuccess || (dw_q == nullptr && dw_k == nullptr)) return e;
   const int k1 = p.n_kinds > 2 ? p.kind[2].block0 : blocks;
   auto kern = bf16 ? dw_reduce_kernel<true> : dw_reduce_kernel<false>;
-  kern<<<dim3(p.d / 32, 2), 1024, 0, st>>>(p.dw_part, p.d, p.kind[0].block0, p.kind[1].block0, k1, p.weight_fp32,
-                                           dw_q, dw_k);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.d / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  // the launch itself overlaps the end of the kernel that leaves the partial rows
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = blocks > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const float*>(p.dw_part), p.d, p.kind[0].block0, p.kind[1].block0,
+                            k1, p.weight_fp32, dw_q, dw_k);
 }
 
 }  // namespace sdpa

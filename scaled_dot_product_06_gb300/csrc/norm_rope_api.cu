@@ -141,9 +141,13 @@ size_t sdpa_qk_norm_rope_bwd_workspace_size(int64_t b, int64_t s, int64_t h, int
   NormRopeParams p{};
   fill_common(&p, b, s, d, 0, 0, nullptr, nullptr, 0, nullptr, 0, 1.f);
   size_t most = 0;
-  for (int kinds = 2; kinds <= 3; ++kinds) {
+  for (int call = 0; call < 6; ++call) {  // with and without values, either weight or both
+    const int kinds = 2 + call / 3, weights = call % 3 + 1;
     p.n_kinds = kinds;
-    for (int i = 0; i < kinds; ++i) p.kind[i].heads = static_cast<int>(i == 0 ? h : h_kv);
+    for (int i = 0; i < kinds; ++i) {
+      p.kind[i].heads = static_cast<int>(i == 0 ? h : h_kv);
+      p.kind[i].weight = (weights >> i) & 1 ? &p : nullptr;  // (whether there is one)
+    }
     const int blocks = empty ? 0 : norm_rope_plan(&p, true);
     if (blocks < 0) return 0;
     const size_t bytes = static_cast<size_t>(blocks) * static_cast<size_t>(d) * sizeof(float);
