@@ -515,8 +515,10 @@ sdpa_status_t sdpa_qk_norm_rope_bwd(int64_t b, int64_t s, int64_t h, int64_t h_k
  *   Heads    h_kv divides h; query head i reads K/V head i / (h / h_kv).
  *   Layout   contiguous, pointers 16-byte aligned, head sizes as elsewhere.
  *   Workspace  sdpa_fwd_prefix_workspace_size(...) bytes, 256-byte aligned:
- *            fp32 partial rows of the key ranges the work is cut into. Two
- *            calls that may run at the same time need one each.
+ *            fp32 partial rows of the key ranges the work is cut into, and a
+ *            counter. Each call clears what it counts with; nothing is kept from
+ *            one call to the next. Two calls that may run at the same time need
+ *            one each.
  * Results are the same bits in every run. b, h or s_q of 0: a no-op.
  */
 size_t sdpa_fwd_prefix_workspace_size(int64_t b, int64_t h, int64_t h_kv, int64_t s_q,

@@ -446,10 +446,12 @@ __device__ __forceinline__ float rcp(float x) {
 // and S'' within cap 2^-29 of the cap. r is off by at most about 2^-21
 // relative (two approximate functions and six roundings), S'' by cap 2^-21.
 // tanh.approx would take one exponential unit slot less a value and leave
-// S'' off by cap 2^-11, which at a cap of 50 is 2.4% of P. An odd polynomial
-// of S' / cap up to 3/4 (four FMAs and a multiply, no exponential unit) did
-// not pay: the softmax warps wait for their own instructions, not for that
-// unit (38% busy), and b4 h16 s2048 d128 took 111 us causal for 108.
+// S'' off by cap 2^-11, which at a cap of 50 is 2.4% of P.
+// The forward's softmax warps, two a scheduler, are what b4 h16 s2048 d128
+// causal waits for (110 us; 82 us without a cap). Tried there: a reciprocal for
+// two values, 114 us; r and the exponential in one loop, 118 us; an odd
+// polynomial of S' / cap up to 3/4 (four FMAs and a multiply, no exponential
+// unit), 111 us, and 122 us where scores are larger.
 // HOLD: with the hold at 30; there a score that is not a number counts as a
 // large one (the backward has such a row's statistics, which are none either).
 template <bool HOLD = true>

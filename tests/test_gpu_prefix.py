@@ -116,7 +116,14 @@ CASES = [
     (1, 8, 8, 1, 40000, 20, [20], 64, 64, "bf16", 0.0),                # a long prefix, many parts
     (5, 10, 2, 1, 0, 9000, [9000, 1, 4097, 8999, 128], 128, 128, "bf16", 0.0),  # long own keys
     (2, 4, 2, 1, 130, 50, [77, -3], 64, 64, "bf16", 0.0),              # lengths outside the cache
-    (2, 4, 2, 5, 5000, 4000, [4000, 3], 192, 128, "bf16", 0.0),        # one stage, fewer keys than tokens
+    (2, 4, 2, 5, 5000, 4000, [4000, 3], 192, 128, "bf16", 0.0),        # fewer keys than tokens
+    (2, 16, 1, 9, 400, 500, [9, 444], 192, 128, "bf16", 0.0),          # row tiles one by one: R = 144
+    (40, 12, 4, 1, 700, 90, list(range(1, 81, 2)), 192, 128, "fp16", 20.0),  # and of the prefix
+    (2, 32, 1, 1, 0, 1100, [1100, 33], 128, 128, "bf16", 0.0),         # R = 32: all lanes of a warp
+    (2, 33, 1, 1, 60, 300, [300, 97], 64, 64, "fp16", 30.0),           # R = 33: one more
+    (200, 8, 1, 1, 0, 900, [900 if i % 37 == 5 else i % 2 for i in range(200)], 64, 64, "bf16", 0.0),  # more
+    # items than CTAs, most of them empty
+    (200, 4, 1, 1, 0, 40, [0] * 200, 64, 64, "bf16", 10.0),            # all of them
 ]
 
 
