@@ -168,6 +168,16 @@ __global__ void __launch_bounds__(384, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    if (p.items_prefix > 0) {
+      tma_prefetch_desc(&tmQp);
+      tma_prefetch_desc(&tmKp);
+      tma_prefetch_desc(&tmVp);
+    }
+    if (p.items_own > 0) {
+      tma_prefetch_desc(&tmQo);
+      tma_prefetch_desc(&tmKo);
+      tma_prefetch_desc(&tmVo);
+    }
     // (a number is read by the MMA issuer and the eight softmax warps)
     for (int i = 0; i < PB_COUNT; ++i) mbar_init(bar(i), (i == PB_P || i == PB_P + 1) ? 128u : i >= PB_IE ? 9u : 1u);
     *abort_flag = 0u;

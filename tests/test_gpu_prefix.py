@@ -231,6 +231,36 @@ def test_two_streams_and_a_graph():
     assert sdpa_device_error() == 0
 
 
+def test_graphs_share_a_workspace():
+    """More items than CTAs (the counter is cleared in the graph): two graphs with
+    one workspace, replayed in turn with other lengths, give the eager calls' bits."""
+    calls, want = [], []
+    b, h, h_kv, s_max, d = 180, 4, 1, 500, 64
+    size = sdpa_fwd_prefix_workspace_size(b, h, h_kv, 1, 300, s_max, d, d)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    for seed in (1, 2):
+        x = make(b, h, h_kv, 1, 300, s_max, d, d, "bf16", [s_max] * b, seed=seed)
+        args = [x[n].cuda() for n in ("q", "kp", "vp", "k", "v", "lens")]
+        out = (torch.empty(b, h, 1, d, dtype=torch.bfloat16, device="cuda"),
+               torch.empty(b, h, 1, device="cuda"))
+        kw = dict(out=out[0], lse=out[1], workspace=ws)
+        sdpa_fwd_prefix(*args, **kw)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            sdpa_fwd_prefix(*args, **kw)
+        calls.append((graph, args, out))
+    for turn in range(3):
+        for graph, args, out in calls:
+            args[5].copy_(torch.tensor([(37 * i + 101 * turn) % (s_max + 1) for i in range(b)]))
+            want.append([t.clone() for t in sdpa_fwd_prefix(*args)])
+            out[0].zero_(), out[1].zero_()
+            graph.replay()
+            assert torch.equal(out[0], want[-1][0]) and torch.equal(out[1], want[-1][1])
+    torch.cuda.synchronize()
+    assert sdpa_device_error() == 0
+
+
 def test_serving_loop_equals_the_whole_sequence():
     """As it is served: the prompt's keys normed, rotated and attended once,
     then tokens normed, rotated, appended and attended one step at a time; each
