@@ -512,7 +512,9 @@ sdpa_status_t sdpa_qk_norm_rope_bwd(int64_t b, int64_t s, int64_t h, int64_t h_k
  *            j <= seqlen_k - s_q + t. A row that sees no key gets O = 0 and
  *            LSE = -inf.
  *            Values of the prefix and inside the lengths must be finite: a key
- *            that a token does not see enters its sum with a weight of 0.
+ *            that a token does not see enters its sum with a weight of 0. Keys
+ *            and queries may be NaN: the rows that see one get NaN in O and LSE,
+ *            no other row does.
  *   scale    as in sdpa_fwd; softcap 0 (none) or as in the capped calls.
  *   Heads    h_kv divides h; query head i reads K/V head i / (h / h_kv).
  *   Layout   contiguous, pointers 16-byte aligned, head sizes as elsewhere.

@@ -1,7 +1,8 @@
 // Joins the partial rows of the shared-prefix attention:
 //   L = log2 sum_s 2^L_s,  O = sum_s 2^(L_s - L) O_s,  LSE = L ln 2
 // over the slots a row has: the prefix's, and as many of the own keys' as its
-// sequence's length fills. A row without a key gets O = 0 and LSE = -inf.
+// sequence's length fills. A row without a key gets O = 0 and LSE = -inf; a row
+// with an L that is not a number (it sees such a score) is none itself.
 // Bound by the latency of reading the partials, which the first kernel has
 // just left in L2: a warp has 8 rows and 32 columns, whose partials are one line
 // a column group (prefix_part_index), and reads 8 slots of them at once; warps
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) 
     for (int i = 0; i < 8; ++i) {
       const float wi = __shfl_sync(0xffffffffu, i < 4 ? w0 : w1, (i & 3) * 8 + (lane & 7));
       l += wi;
-      const bool some = wi > 0.f;
+      const bool some = wi > 0.f;  // (not a number: O_s is not there, the row is none by the weight)
       a0.x = fmaf(wi, some ? v0[i].x : 0.f, a0.x), a0.y = fmaf(wi, some ? v0[i].y : 0.f, a0.y);
       a0.z = fmaf(wi, some ? v0[i].z : 0.f, a0.z), a0.w = fmaf(wi, some ? v0[i].w : 0.f, a0.w);
       a1.x = fmaf(wi, some ? v1[i].x : 0.f, a1.x), a1.y = fmaf(wi, some ? v1[i].y : 0.f, a1.y);
@@ -106,11 +107,11 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) 
     }
   }
   if (!live) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.o) + row * DV * 2);
   dst[c0] = make_uint2(pack2<BF16>(a0.x * inv, a0.y * inv), pack2<BF16>(a0.z * inv, a0.w * inv));
   dst[c0 + 4] = make_uint2(pack2<BF16>(a1.x * inv, a1.y * inv), pack2<BF16>(a1.z * inv, a1.w * inv));
-  if (c0 == 0) p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : SDPA_NEG_INF;
+  if (c0 == 0) p.lse[row] = l == 0.f ? SDPA_NEG_INF : (m + __log2f(l)) * kLn2;
 }
 
 template <bool BF16, int DV>

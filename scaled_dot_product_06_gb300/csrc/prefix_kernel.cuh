@@ -540,7 +540,9 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
       }
-      if (row_ok) p.part_lse[at] = l > 0.f ? m + __log2f(l) + p.lse_shift : SDPA_NEG_INF;
+      // (a sum that is not a number leaves an L that is none: the join then makes the
+      // row none, without reading the partial, which is not stored)
+      if (row_ok) p.part_lse[at] = l == 0.f ? SDPA_NEG_INF : m + __log2f(l) + p.lse_shift;
       tc_fence_before();  // O has been read before the next item's P is announced
     }
   }
