@@ -3,6 +3,12 @@
 PyTorch provides device memory and the stream; every step of the attention
 computation runs in libsdpa.so's kernels. The functions here only check
 tensor properties, allocate outputs with torch and pass raw pointers.
+
+Every call runs on ``stream``, by default the current one. What it allocates
+(outputs and workspace that are not given) is then that stream's, as within
+``torch.cuda.stream(stream)``; ordering it behind the work that makes the inputs,
+and the readers of the outputs behind it, is the caller's part, and so is
+keeping the inputs until it has run.
 """
 from __future__ import annotations
 
@@ -25,10 +31,32 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream_ptr(stream, t: torch.Tensor) -> int:
     if stream is not None:
+        if getattr(stream, "device", t.device) != t.device:
+            raise ValueError("stream must be one of the tensors' device")
         return int(stream.cuda_stream)
     if _raw_stream is not None:
         return int(_raw_stream(t.get_device()))
     return int(torch.cuda.current_stream(t.device).cuda_stream)
+
+
+def new_tensor(shape, dtype, device, stream, scratch=False) -> torch.Tensor:
+    """Memory for a call on ``stream`` (None: the current one).
+
+    The allocator hands memory out in the order of the stream it is asked on:
+    memory of the current stream's could still be in use there when ``stream``
+    writes it, and a dropped workspace would be given to the next call while
+    ``stream`` works in it. So it is asked on ``stream``. Outputs are noted as used
+    by the caller's stream too: dropped, they wait for its work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch and stream != caller:
+        t.record_stream(caller)
+    return t
 
 
 def _check_io(name: str, t: torch.Tensor, shape, dtype) -> None:
@@ -127,9 +155,9 @@ def sdpa_fwd(q, k, v, *, scale=None, is_causal=False, dropout_p=0.0, seed=0, off
         _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
     if out is None:
-        out = torch.empty((b, h, s_q, d_v), dtype=dt, device=q.device)
+        out = new_tensor((b, h, s_q, d_v), dt, q.device, stream)
     if lse is None:
-        lse = torch.empty((b, h, s_q), dtype=torch.float32, device=q.device)
+        lse = new_tensor((b, h, s_q), torch.float32, q.device, stream)
     _check_io("out", out, (b, h, s_q, d_v), dt)
     _check_io("lse", lse, (b, h, s_q), torch.float32)
     cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask)
@@ -212,14 +240,14 @@ def sdpa_bwd_phases(phases, q, k, v, o, dout, lse, *, scale=None, is_causal=Fals
     if bias is not None:
         _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = new_tensor(q.shape, dt, q.device, stream) if dq is None else dq
+    dk = new_tensor(k.shape, dt, q.device, stream) if dk is None else dk
+    dv = new_tensor(v.shape, dt, q.device, stream) if dv is None else dv
     if bias is not None and dbias is None:
-        dbias = torch.empty_like(bias)
+        dbias = new_tensor(bias.shape, torch.float32, q.device, stream)
     need = sdpa_bwd_workspace_size(b, h, s_q, s_kv, d_qk, d_v, h_kv, deterministic)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = new_tensor(max(need, 1), torch.uint8, q.device, stream, scratch=True)
     cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask)
     if cap is not None:
         st = _native.lib().sdpa_bwd_phases_capped(
@@ -276,9 +304,9 @@ def sdpa_fwd_varlen(q, k, v, seqstart_q, seqstart_k, max_seqlen_q, max_seqlen_k,
     _check_io("v", v, (h_kv, total_k, d_v), dt)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
     if out is None:
-        out = torch.empty((h, total_q, d_v), dtype=dt, device=q.device)
+        out = new_tensor((h, total_q, d_v), dt, q.device, stream)
     if lse is None:
-        lse = torch.empty((h, total_q), dtype=torch.float32, device=q.device)
+        lse = new_tensor((h, total_q), torch.float32, q.device, stream)
     _check_io("out", out, (h, total_q, d_v), dt)
     _check_io("lse", lse, (h, total_q), torch.float32)
     cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask)
@@ -362,12 +390,12 @@ def sdpa_bwd_phases_varlen(phases, q, k, v, o, dout, lse, seqstart_q, seqstart_k
         _check_io(name, t, shp, dt)
     _check_io("lse", lse, (h, total_q), torch.float32)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = new_tensor(q.shape, dt, q.device, stream) if dq is None else dq
+    dk = new_tensor(k.shape, dt, q.device, stream) if dk is None else dk
+    dv = new_tensor(v.shape, dt, q.device, stream) if dv is None else dv
     need = sdpa_bwd_varlen_workspace_size(b, h, total_q, d_qk, deterministic)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = new_tensor(max(need, 1), torch.uint8, q.device, stream, scratch=True)
     cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask)
     if cap is not None:
         st = _native.lib().sdpa_bwd_phases_varlen_capped(
@@ -403,7 +431,7 @@ def sdpa_dropout_mask(b, h, s_q, s_kv, dropout_p, seed, offset, device="cuda", s
     ``out`` when given). Passed back as ``dropout_mask``, the attention calls
     read these bits instead of drawing them."""
     words = (b * h * s_q * s_kv + 31) // 32
-    bits = torch.empty(max(words, 1), dtype=torch.int32, device=device) if out is None else out
+    bits = new_tensor(max(words, 1), torch.int32, device, stream) if out is None else out
     if out is not None and (out.dtype != torch.int32 or out.numel() < words or not out.is_cuda):
         raise ValueError(f"out must be an int32 CUDA tensor of at least {words} words")
     st = _native.lib().sdpa_dropout_mask(b, h, s_q, s_kv, float(dropout_p), int(seed), int(offset),

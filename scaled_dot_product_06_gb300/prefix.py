@@ -7,7 +7,7 @@ import math
 import torch
 
 from . import _native
-from .api import _DTYPE_CODE, _stream_ptr
+from .api import _DTYPE_CODE, _stream_ptr, new_tensor
 from .rows import check_flat, on_device
 
 
@@ -51,14 +51,14 @@ def sdpa_fwd_prefix(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, softc
     v_p = check_flat("v", v, (b, h_kv, s_max, d_v), dt, dev)
     n_p = check_flat("seqlens_k", seqlens_k, (b,), torch.int32, dev)
     if out is None:
-        out = torch.empty((b, h, s_q, d_v), dtype=dt, device=dev)
+        out = new_tensor((b, h, s_q, d_v), dt, dev, stream)
     if lse is None:
-        lse = torch.empty((b, h, s_q), dtype=torch.float32, device=dev)
+        lse = new_tensor((b, h, s_q), torch.float32, dev, stream)
     o_p = check_flat("out", out, (b, h, s_q, d_v), dt, dev)
     l_p = check_flat("lse", lse, (b, h, s_q), torch.float32, dev)
     if workspace is None:
-        workspace = torch.empty(max(_bytes(b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v), 1),
-                                dtype=torch.uint8, device=dev)
+        workspace = new_tensor(max(_bytes(b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v), 1), torch.uint8, dev,
+                               stream, scratch=True)
     with on_device(q):
         st = _native.lib().sdpa_fwd_prefix(
             b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v, 1.0 / math.sqrt(d_qk) if scale is None else scale,

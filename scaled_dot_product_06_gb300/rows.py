@@ -13,7 +13,7 @@ import struct
 import torch
 
 from . import _native
-from .api import _DTYPE_CODE, _ptr, _stream_ptr
+from .api import _DTYPE_CODE, _ptr, _stream_ptr, new_tensor
 
 _NO_GUARD = contextlib.nullcontext()
 _pack_rows = struct.Struct("Pqqq").pack  # the bytes of an sdpa_rows_t
@@ -138,13 +138,13 @@ def sdpa_qk_norm_rope(q, k, cos, sin, *, v=None, positions=None, q_weight=None, 
     # outputs: new ones are contiguous
     row, kv_shape = d, (b, h_kv, cache, d)
     if q_out is None:
-        q_out = torch.empty((b, h, s, d), dtype=dt, device=dev)
+        q_out = new_tensor((b, h, s, d), dt, dev, stream)
         q_to = _pack_rows(q_out.data_ptr(), h * s * row, row, s * row)
     else:
         q_to = _head_rows("q_out", q_out, (b, h, s, d), dt, dev)
         _check_output("q_out", q_out)
     if k_out is None:
-        k_out = torch.empty(kv_shape, dtype=dt, device=dev)
+        k_out = new_tensor(kv_shape, dt, dev, stream)
         k_to = _pack_rows(k_out.data_ptr(), h_kv * s * row, row, s * row)
     else:
         k_to = _head_rows("k_out", k_out, kv_shape, dt, dev)
@@ -152,7 +152,7 @@ def sdpa_qk_norm_rope(q, k, cos, sin, *, v=None, positions=None, q_weight=None, 
     v_to = None
     if v is not None:
         if v_out is None:
-            v_out = torch.empty((b, h_kv, s, d_v), dtype=dt, device=dev)
+            v_out = new_tensor((b, h_kv, s, d_v), dt, dev, stream)
         else:
             _check_output("v_out", v_out)
         v_to = _head_rows("v_out", v_out, (b, h_kv, cache, d_v), dt, dev)
@@ -200,13 +200,12 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos, sin, *, dv_out=None, positi
     gv = None if dv_out is None else _head_rows("dv_out", dv_out, (b, h_kv, s, d_v), dt, dev)
     rot, cos_p, sin_p, n_pos, pos_p = _table(dev, cos, sin, positions, b, s)
     qw_p, kw_p, fp32 = _weights(dt, dev, q_weight, k_weight, d)
-    new = functools.partial(torch.empty, dtype=dt, device=dev)
     if dq is None:
-        dq = new((b, s, h, d))
+        dq = new_tensor((b, s, h, d), dt, dev, stream)
     if dk is None:
-        dk = new((b, s, h_kv, d))
+        dk = new_tensor((b, s, h_kv, d), dt, dev, stream)
     if dv is None and dv_out is not None:
-        dv = new((b, s, h_kv, d_v))
+        dv = new_tensor((b, s, h_kv, d_v), dt, dev, stream)
     for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         if t is not None:
             _check_output(name, t)
@@ -219,12 +218,12 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos, sin, *, dv_out=None, positi
             if g is not None:
                 raise ValueError(f"{name} without its weight")
         elif g is None:
-            g = torch.empty_like(w)
+            g = new_tensor((d,), w.dtype, dev, stream)
         else:
             check_flat(name, g, (d,), w.dtype, dev)
         grads.append(g)
     if workspace is None and (q_weight is not None or k_weight is not None):
-        workspace = torch.empty(max(_bwd_bytes(b, s, h, h_kv, d, d_v), 1), dtype=torch.uint8, device=dev)
+        workspace = new_tensor(max(_bwd_bytes(b, s, h, h_kv, d, d_v), 1), torch.uint8, dev, stream, scratch=True)
     with on_device(q):
         st = _native.lib().sdpa_qk_norm_rope_bwd(
             b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], gq, gk, gv, q_in, k_in, q_to, k_to, v_to, rot,
