@@ -421,7 +421,15 @@ __global__ void __launch_bounds__(384, 1)
         tmem_wait_ld();
         float mx = SDPA_NEG_INF;
         const bool hidden = k0 + N - 1 > all_see;  // there are hidden keys
-        if constexpr (CAP) mx = cap_scores<N>(xs, p.cap_in, sl2, row_ok);
+        if constexpr (CAP) {
+          // scores share reciprocals: what lies behind the last key must not lend its roundings
+          if (k0 + N > it.keys) {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+              if (k0 + e >= it.keys) xs[e] = 0.f;
+          }
+          mx = cap_scores<N>(xs, p.cap_in, sl2, row_ok);
+        }
         if (hidden) {
 #pragma unroll
           for (int e = 0; e < N; ++e)
