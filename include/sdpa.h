@@ -27,7 +27,8 @@
  *   Causal      Top-left: key j is visible to query i iff j <= i.
  *   LSE         Natural-log logsumexp of the scaled, biased, masked scores
  *               before dropout; -inf for a row that sees no key (its O row
- *               is 0 and it adds nothing to any gradient).
+ *               is 0 and it adds nothing to any gradient). A row with a
+ *               visible score that is NaN, or +inf, has NaN in O and LSE.
  *   Dropout     p in [0, 1); p == 0 disables it and seed/offset are ignored.
  *               Element (b,h,i,j) has linear index L = ((b*h_n+h)*s_q+i)*s_kv+j;
  *               its 32-bit draw r is word L%4 of Philox4x32-10 with key

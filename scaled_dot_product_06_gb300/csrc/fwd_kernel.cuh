@@ -539,7 +539,9 @@ __global__ void __launch_bounds__(384, 1)
     // ---- epilogue: O / l (times 1/(1-p) under dropout), LSE = m ln2 + ln l
     if (n_kv > 0 && ok && mbar_wait(bar(FB_O + t), 0, ec, kSiteFwdSoftmax)) {
       tc_fence_after();
-      const float inv = (l > 0.f) ? (DROP ? p.keep_scale : 1.0f) / l : 0.f;
+      // (l is 0 in a row that sees no key alone; not a number where a visible score is
+      // none, and then O and LSE are none, dropped entries of P or not)
+      const float inv = (l == 0.f) ? 0.f : (DROP ? p.keep_scale : 1.0f) / l;
       const size_t ri = static_cast<size_t>(zq) * p.rows_q + sl.row_q + (row_ok ? row : 0);
       uint8_t* orow = static_cast<uint8_t*>(p.o) + ri * DV * 2;
 #pragma unroll
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (row_ok)
-        p.lse[ri] = (l > 0.f) ? fmaf(m, kLn2, __logf(l)) + (CAP ? p.softcap : 0.f) : SDPA_NEG_INF;
+        p.lse[ri] = (l == 0.f) ? SDPA_NEG_INF : fmaf(m, kLn2, __logf(l)) + (CAP ? p.softcap : 0.f);
     } else if (n_kv == 0 && row_ok && !(t == 1 && lone)) {
       // no row of this tile sees a key (the other tile's rows do): O = 0, LSE = -inf
       // (a lone tile 0's partner rows belong to the next pair)
