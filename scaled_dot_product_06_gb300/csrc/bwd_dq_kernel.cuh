@@ -457,13 +457,9 @@ __global__ void __launch_bounds__(DqCfg<DQK, DV>::THREADS, 1)
       if (!(ok = mbar_wait(bar(QB_S), j & 1, ec, kSiteBwdCompute))) break;
       tc_fence_after();
       if constexpr (CAP) {  // pr = P (1 - tanh^2); P itself is not needed here
-        tmem_ld32f(tbase + C::T_S + lane_off + CW * hf, pr);
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(bar(QB_SFREE));
         uint32_t pwc[16];
-        cap_probs<BF16>(pr, pwc, p.cap_in, p.cap_out, [&](int) { return make_float4(nl2, nl2, nl2, nl2); },
-                        [](int) { return 1.0f; });
+        cap_probs<BF16>(tbase + C::T_S + lane_off + CW * hf, bar(QB_SFREE), pr, pwc, p.cap_in, p.cap_out,
+                        [&](int) { return make_float4(nl2, nl2, nl2, nl2); }, [](int) { return 1.0f; });
         const Band wb = lds_band(band_slot);
         if ((kc0 + CW > S_kv) || (kc0 + CW - 1 > q0 + wb.hi) || (kc0 < q0 + BM - 1 + wb.lo) || !row_ok) {
           const int first = qr + wb.lo;  // the row's visible keys, none past S_q

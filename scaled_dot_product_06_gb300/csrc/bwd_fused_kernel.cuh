@@ -547,11 +547,8 @@ __global__ void __launch_bounds__(FusedCfg<DQK, DV>::THREADS, 1)
         // CAP: P packed for dV (pwc) and pr = P (1 - tanh^2)
         uint32_t pwc[16];
         if constexpr (CAP) {
-          tmem_ld32f(tcs, pr);
-          tmem_wait_ld();
-          tc_fence_before();
-          mbar_arrive(bar(FB_SFREE));  // S^T(i) is in registers
-          cap_probs<BF16>(pr, pwc, p.cap_in, p.cap_out, [&](int e4) { return lds128(nl2_s + 16u * e4); }, zf);
+          cap_probs<BF16>(tcs, bar(FB_SFREE), pr, pwc, p.cap_in, p.cap_out,
+                          [&](int e4) { return lds128(nl2_s + 16u * e4); }, zf);
           const Band wb = lds_band(band_slot);
           if ((qc0 < k0 + C::BN - 1 - wb.hi) || (qc0 + CW - 1 > k0 - wb.lo) || (qc0 + CW > S_q) || !kv_ok) {
             const int first = kv - wb.hi - qc0;  // visible local columns [first, lim)

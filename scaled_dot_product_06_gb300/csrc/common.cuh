@@ -434,17 +434,20 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // Capped scores: S'' = cap tanh(S' / cap), S' = scale S. With
-//   r = 1 / (1 + e^(2 S' / cap)):   tanh(S' / cap) = 1 - 2 r,
-//   S'' = cap - 2 cap r,            1 - tanh^2 = 4 r (1 - r),
-// so r is all the kernels need: the exponent of the softmax is one FMA of it,
-// and the backward's factor keeps its relative precision where tanh saturates.
+//   e = e^(2 S' / cap), r = 1 / (1 + e):   tanh(S' / cap) = 1 - 2 r,
+//   S'' = cap - 2 cap r,                   1 - tanh^2 = 4 r (1 - r) = 4 e r^2,
+// so r is all the forward needs (the exponent of the softmax is one FMA of it),
+// and r and e the backward: 4 e r^2 has a small relative error wherever tanh
+// saturates, where 4 r (1 - r) would lose it below, as r comes near 1.
 // Takes x[0, 8) raw scores S to r, c = 2 log2(e) scale / cap. The exponential
 // unit bounds these kernels, so four values share one reciprocal: with
 // a_i = 1 + e_i, 1 / a_0 = a_1 (a_2 a_3) / (a_0 a_1 a_2 a_3) and so on (2.25
 // multiplies and a quarter of a reciprocal a value). The exponent is held to
 // 30 so that the product of four stays below 2^121; there r is under 2^-29
-// and S'' within cap 2^-29 of the cap. r is off by at most about 2^-21
-// relative (two approximate functions and six roundings), S'' by cap 2^-21.
+// and S'' within cap 2^-29 of the cap. r is off by at most 2^-21 relative
+// (seven units of 2^-24: five roundings and the reciprocal's ulp, besides 2^-22
+// of the exponential's where e counts), S'' by cap 2^-20: the most where r is
+// near 1, at the negative cap.
 // tanh.approx would take one exponential unit slot less a value and leave
 // S'' off by cap 2^-11, which at a cap of 50 is 2.4% of P.
 // The forward's softmax warps, two a scheduler, are what b4 h16 s2048 d128
@@ -454,15 +457,20 @@ __device__ __forceinline__ float rcp(float x) {
 // unit), 111 us, and 122 us where scores are larger.
 // HOLD: with the hold at 30; there a score that is not a number counts as a
 // large one (the backward has such a row's statistics, which are none either).
-template <bool HOLD = true>
-__device__ __forceinline__ void cap_r8(float* x, float c) {
-  auto held = [](float y) { return HOLD ? fminf(y, 30.f) : y; };
+// FACTOR: fac[0, 8) = 4 e r^2; the exponential is then taken of the exponent
+// plus 2, which costs nothing.
+template <bool HOLD = true, bool FACTOR = false>
+__device__ __forceinline__ void cap_r8(float* x, float c, float* fac = nullptr) {
+  constexpr float kHold = FACTOR ? 32.f : 30.f;
+  auto held = [](float y) { return HOLD ? fminf(y, kHold) : y; };
   const uint64_t c2 = f2(c, c), one = f2(1.f, 1.f);
-  uint64_t a[4];
+  uint64_t a[4], e[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 y = f2split(mul2(f2(x[2 * i], x[2 * i + 1]), c2));
-    a[i] = add2(f2(ex2(held(y.x)), ex2(held(y.y))), one);
+    const uint64_t s = f2(x[2 * i], x[2 * i + 1]);
+    const float2 y = f2split(FACTOR ? fma2(s, c2, f2(2.f, 2.f)) : mul2(s, c2));
+    e[i] = f2(ex2(held(y.x)), ex2(held(y.y)));
+    a[i] = FACTOR ? fma2(e[i], f2(0.25f, 0.25f), one) : add2(e[i], one);
   }
   const uint64_t p01 = mul2(a[0], a[1]), p23 = mul2(a[2], a[3]);
   const float2 all = f2split(mul2(p01, p23));
@@ -474,6 +482,11 @@ __device__ __forceinline__ void cap_r8(float* x, float c) {
     const float2 v = f2split(r[i]);
     x[2 * i] = v.x;
     x[2 * i + 1] = v.y;
+    if constexpr (FACTOR) {
+      const float2 f = f2split(mul2(mul2(e[i], r[i]), r[i]));
+      fac[2 * i] = f.x;
+      fac[2 * i + 1] = f.y;
+    }
   }
 }
 
@@ -528,19 +541,45 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   }
 }
 
-// Capped scores, backward: raw scores s[0, 32) of one thread's columns to P
-// and P (1 - tanh^2). The exponent is cap_out r + n (n: the statistic, which
-// holds -LSE log2e + softcap log2e), 1 - tanh^2 = 4 r (1 - r). P leaves
-// packed for the dV product (times the dropout factor zf), so that the
-// fp32 registers hold only P (1 - tanh^2), which the softmax backward
-// multiplies by dP - D. Columns outside [first, lim) are masked to zero by
-// selection: P of a hidden score may be infinite.
+// Capped scores, backward: reads one thread's 32 raw scores at `tcol` in tensor
+// memory, releases them (an arrival at `sfree`), and leaves P and P (1 - tanh^2)
+// of them. The exponent is cap_out r + n (n: the statistic, which holds -LSE
+// log2e + softcap log2e). P leaves packed for the dV product (times the dropout
+// factor zf), so that the fp32 registers hold only P (1 - tanh^2), which the
+// softmax backward multiplies by dP - D. Columns outside [first, lim) are masked
+// to zero by selection: P of a hidden score may be infinite.
+// 1 - tanh^2 is 4 r (1 - r) where the exponents of the warp's scores lie within
+// 12 (bf16: |S'| <= 4.1 cap) or 9 (fp16: 3.1 cap): r's 2^-21 is there at most
+// 2^-9 or 2^-12 of 1 - r, half of what rounding dS adds, and no hold is needed.
+// Elsewhere cap_r8 forms it from e as well. A thread whose scores lie within
+// releases them at once; the others' stay, and are read again after the usual
+// way has run for nothing. Measured on the whole backward of b4 h16 s2048 d128
+// causal: 268 us, where 4 r (1 - r) everywhere takes 262, the factor from e
+// everywhere 289 (its registers spill), a choice ahead of both ways 283, and the
+// smallest and the largest score instead of the largest |score| 268, but 290 for 277
+// in the deterministic backward. (b8 h16 s2048 d64 fp16: 393 us for 382, and 470
+// where nearly every warp has a score that needs it.)
 template <bool BF16, typename Stat, typename Zf>
-__device__ __forceinline__ void cap_probs(float (&s)[32], uint32_t (&pw)[16], float cap_in, float cap_out,
-                                          Stat stat4, Zf zf) {
+__device__ __forceinline__ void cap_probs(uint32_t tcol, uint32_t sfree, float (&s)[32], uint32_t (&pw)[16],
+                                          float cap_in, float cap_out, Stat stat4, Zf zf) {
+  const uint64_t co2 = f2(cap_out, cap_out);
+  tmem_ld32f(tcol, s);
+  tmem_wait_ld();
+  // the largest |score| in a tree of four steps: the release waits for it
+  float b[4];
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) cap_r8(s + i, cap_in);
-  const uint64_t co2 = f2(cap_out, cap_out), four = f2(4.f, 4.f), mfour = f2(-4.f, -4.f);
+  for (int i = 0; i < 4; ++i) {
+    const float* x = s + 8 * i;
+    b[i] = fmax3_nan(fmax3_nan(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])),
+                     fmax3_nan(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmax3_nan(fabsf(x[6]), fabsf(x[7]), 0.f));
+  }
+  const float big = fmax3_nan(fmax3_nan(b[0], b[1], b[2]), b[3], b[3]);
+  const bool near = big * fabsf(cap_in) <= (BF16 ? 12.f : 9.f);
+  tc_fence_before();
+  mbar_arrive_if(sfree, near);
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) cap_r8<false>(s + i, cap_in);
+  const uint64_t four = f2(4.f, 4.f), mfour = f2(-4.f, -4.f);
 #pragma unroll
   for (int e4 = 0; e4 < 8; ++e4) {
     const float4 n4 = stat4(e4);
@@ -555,6 +594,41 @@ __device__ __forceinline__ void cap_probs(float (&s)[32], uint32_t (&pw)[16], fl
       s[c] = g.x;
       s[c + 1] = g.y;
     }
+  }
+  if (!__all_sync(0xffffffffu, near)) {
+    // (a loop over 16 columns, through local memory: registers and instructions of
+    // the other way are not to pay for this one)
+    float gl[32];
+    uint32_t pl[16];
+#pragma unroll 1
+    for (int i = 0; i < 32; i += 16) {
+      uint32_t raw[16];
+      tmem_ld16(tcol + i, raw);
+      tmem_wait_ld();
+#pragma unroll
+      for (int o = 0; o < 16; o += 8) {
+        float r[8], f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = __uint_as_float(raw[o + e]);
+        cap_r8<true, true>(r, cap_in, f);
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 n4 = stat4((i + o + e) / 4);
+          const float p0 = ex2(fmaf(r[e], cap_out, n4.x)), p1 = ex2(fmaf(r[e + 1], cap_out, n4.y));
+          const float p2 = ex2(fmaf(r[e + 2], cap_out, n4.z)), p3 = ex2(fmaf(r[e + 3], cap_out, n4.w));
+          const int c = i + o + e;
+          pl[c / 2] = pack2<BF16>(p0 * zf(c), p1 * zf(c + 1));
+          pl[c / 2 + 1] = pack2<BF16>(p2 * zf(c + 2), p3 * zf(c + 3));
+          gl[c] = p0 * f[e], gl[c + 1] = p1 * f[e + 1], gl[c + 2] = p2 * f[e + 2], gl[c + 3] = p3 * f[e + 3];
+        }
+      }
+    }
+    tc_fence_before();
+    mbar_arrive_if(sfree, !near);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) s[c] = gl[c];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) pw[c] = pl[c];
   }
 }
 
