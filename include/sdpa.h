@@ -394,7 +394,9 @@ sdpa_status_t sdpa_bwd_phases_varlen_ex(
  *     S'' = softcap * tanh(S' / softcap),   S' = scale * Q K^T
  * (masks apply afterwards), and in the backward dS' = dS'' (1 - (S''/softcap)^2).
  *   softcap  in (0, 4096], with scale / softcap finite: SDPA_ERR_INVALID_ARG
- *            otherwise. S'' is formed to softcap * 2^-21.
+ *            otherwise. S'' is formed to softcap * 2^-20 (P to that, relative:
+ *            less than P's own rounding up to a softcap of 512 in fp16, 4096
+ *            in bf16).
  * The windows, the alignment, keep_bits, dropout, grouped heads, packed
  * sequences, workspaces and phases are those of the sdpa_*_ex calls; there is
  * no bias and no ALiBi. One call does the whole backward with SDPA_BWD_ALL.

@@ -294,8 +294,9 @@ sdpa_status_t check_alibi(const Mask& mk, int64_t b, int64_t h) {
 
 // The cap of a capped call: in (0, kMaxSoftcap], with a slope scale / softcap
 // whose product with 2 log2(e) is finite. The kernels form the capped score as
-// softcap - 2 softcap r with r off by 2^-21 relative, so above 4096 the score
-// would be off by more than 2^-9, half a bf16 rounding of P.
+// softcap - 2 softcap r with r in (0, 1) off by 2^-21 relative, so above 4096
+// the score would be off by more than 2^-8, which is a bf16 rounding of P (of
+// fp16's, 2^-11, it is more above 512).
 constexpr float kMaxSoftcap = 4096.f;
 sdpa_status_t check_softcap(const Mask& mk, float scale) {
   if (!mk.capped) return SDPA_OK;
