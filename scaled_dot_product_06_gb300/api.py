@@ -60,14 +60,22 @@ def new_tensor(shape, dtype, device, stream, scratch=False) -> torch.Tensor:
 
 
 def _check_io(name: str, t: torch.Tensor, shape, dtype) -> None:
+    if t.is_cuda and t.shape == shape and t.dtype == dtype and t.is_contiguous():
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (BHSD)")
+    raise ValueError(f"{name} must be contiguous (BHSD)")
+
+
+def check_workspace(t: torch.Tensor, device):
+    """(pointer, bytes) of a workspace that is one block of memory of this device."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of q")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _ptr(t):
@@ -76,18 +84,19 @@ def _ptr(t):
 
 
 def _window(is_causal, window, bottom_right, alibi_slopes, n_batch, h, dropout_mask=None,
-            force=False):
+            force=False, words=0):
     """(left, right, bottom_right, slopes pointer, slope stride, keep-bits
     pointer) for the *_ex entry points, or None for the plain causal / unmasked
     calls (unless force). alibi_slopes: fp32 CUDA [h] (every batch entry) or
     [n_batch, h]; dropout_mask: the int32 words of sdpa_dropout_mask (or of a
-    forward's dropout_mask_out) for the same problem."""
+    forward's dropout_mask_out) for the same problem, `words` of them."""
     if (window is None and not bottom_right and alibi_slopes is None and dropout_mask is None
             and not force):
         return None
     if dropout_mask is not None and (not dropout_mask.is_cuda or dropout_mask.dtype != torch.int32
-                                     or not dropout_mask.is_contiguous()):
-        raise ValueError("dropout_mask must be the contiguous int32 CUDA words of sdpa_dropout_mask")
+                                     or not dropout_mask.is_contiguous() or dropout_mask.numel() < words):
+        raise ValueError(f"dropout_mask must be the contiguous int32 CUDA words of sdpa_dropout_mask, "
+                         f"{words} of them")
     left, right = window if window is not None else (-1, 0 if is_causal else -1)
     stride = 0
     if alibi_slopes is not None:
@@ -104,7 +113,7 @@ def _window(is_causal, window, bottom_right, alibi_slopes, n_batch, h, dropout_m
     return int(left), int(right), int(bool(bottom_right)), _ptr(alibi_slopes), stride, _ptr(dropout_mask)
 
 
-def _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, n_batch, h, dropout_mask):
+def _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, n_batch, h, dropout_mask, words):
     """(softcap, left, right, bottom_right, keep-bits pointer) for the *_capped
     entry points, or None for uncapped scores (softcap None or 0)."""
     if softcap is None or softcap == 0:
@@ -112,8 +121,13 @@ def _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, n_batc
     if bias is not None or alibi_slopes is not None:
         raise ValueError("softcap takes no bias and no alibi_slopes")
     left, right, br, _, _, keep = _window(is_causal, window, bottom_right, None, n_batch, h,
-                                          dropout_mask, force=True)
+                                          dropout_mask, force=True, words=words)
     return float(softcap), left, right, br, keep
+
+
+def _words(dropout_p, b, h, s_q, s_kv) -> int:
+    """Words of a problem's keep bits (0 without dropout, when none are read or written)."""
+    return (b * h * s_q * s_kv + 31) // 32 if dropout_p > 0 else 0
 
 
 def _mask_out(t, words):
@@ -160,7 +174,9 @@ def sdpa_fwd(q, k, v, *, scale=None, is_causal=False, dropout_p=0.0, seed=0, off
         lse = new_tensor((b, h, s_q), torch.float32, q.device, stream)
     _check_io("out", out, (b, h, s_q, d_v), dt)
     _check_io("lse", lse, (b, h, s_q), torch.float32)
-    cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask)
+    words = _words(dropout_p, b, h, s_q, s_kv)
+    cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask,
+                  words)
     if cap is not None:
         rec = _mask_out(dropout_mask_out, (b * h * s_q * s_kv + 31) // 32)
         st = _native.lib().sdpa_fwd_capped(b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *cap, rec,
@@ -170,7 +186,7 @@ def sdpa_fwd(q, k, v, *, scale=None, is_causal=False, dropout_p=0.0, seed=0, off
         _native.check(st, "sdpa_fwd_capped")
         return out, lse
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask,
-                force=dropout_mask_out is not None)
+                force=dropout_mask_out is not None, words=words)
     if w is None:
         st = _native.lib().sdpa_fwd_gqa(b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, int(bool(is_causal)),
                                         float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt],
@@ -243,33 +259,40 @@ def sdpa_bwd_phases(phases, q, k, v, o, dout, lse, *, scale=None, is_causal=Fals
     dq = new_tensor(q.shape, dt, q.device, stream) if dq is None else dq
     dk = new_tensor(k.shape, dt, q.device, stream) if dk is None else dk
     dv = new_tensor(v.shape, dt, q.device, stream) if dv is None else dv
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _check_io(name, t, like.shape, dt)
     if bias is not None and dbias is None:
         dbias = new_tensor(bias.shape, torch.float32, q.device, stream)
+    if dbias is not None:
+        _check_io("dbias", dbias, (1, h, s_q, s_kv), torch.float32)
     need = sdpa_bwd_workspace_size(b, h, s_q, s_kv, d_qk, d_v, h_kv, deterministic)
     if workspace is None:
         workspace = new_tensor(max(need, 1), torch.uint8, q.device, stream, scratch=True)
-    cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask)
+    ws = check_workspace(workspace, q.device)
+    words = _words(dropout_p, b, h, s_q, s_kv)
+    cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask,
+                  words)
     if cap is not None:
         st = _native.lib().sdpa_bwd_phases_capped(
             int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *cap, float(dropout_p), int(seed),
             int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
-            _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _stream_ptr(stream, q))
+            _ptr(dq), _ptr(dk), _ptr(dv), *ws, _stream_ptr(stream, q))
         _native.check(st, "sdpa_bwd_phases_capped")
         return dq, dk, dv, None
-    w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask)
+    w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask, words=words)
     if w is None:
         st = _native.lib().sdpa_bwd_phases_gqa(
             int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, int(bool(is_causal)),
             float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v),
             _ptr(bias), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias),
-            _ptr(workspace), workspace.numel(), _stream_ptr(stream, q))
+            *ws, _stream_ptr(stream, q))
         _native.check(st, "sdpa_bwd_phases_gqa")
     else:
         st = _native.lib().sdpa_bwd_phases_ex(
             int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *w, float(dropout_p), int(seed),
             int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v), _ptr(bias), _ptr(o),
-            _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(workspace),
-            workspace.numel(), _stream_ptr(stream, q))
+            _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias), *ws,
+            _stream_ptr(stream, q))
         _native.check(st, "sdpa_bwd_phases_ex")
     return dq, dk, dv, dbias
 
@@ -309,7 +332,9 @@ def sdpa_fwd_varlen(q, k, v, seqstart_q, seqstart_k, max_seqlen_q, max_seqlen_k,
         lse = new_tensor((h, total_q), torch.float32, q.device, stream)
     _check_io("out", out, (h, total_q, d_v), dt)
     _check_io("lse", lse, (h, total_q), torch.float32)
-    cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask)
+    words = _words(dropout_p, b, h, int(max_seqlen_q), int(max_seqlen_k))
+    cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask,
+                  words)
     if cap is not None:
         rec = _mask_out(dropout_mask_out, (b * h * int(max_seqlen_q) * int(max_seqlen_k) + 31) // 32)
         st = _native.lib().sdpa_fwd_varlen_capped(
@@ -319,7 +344,7 @@ def sdpa_fwd_varlen(q, k, v, seqstart_q, seqstart_k, max_seqlen_q, max_seqlen_k,
         _native.check(st, "sdpa_fwd_varlen_capped")
         return out, lse
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask,
-                force=dropout_mask_out is not None)
+                force=dropout_mask_out is not None, words=words)
     if w is None:
         st = _native.lib().sdpa_fwd_varlen(
             b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v, scale,
@@ -393,25 +418,30 @@ def sdpa_bwd_phases_varlen(phases, q, k, v, o, dout, lse, seqstart_q, seqstart_k
     dq = new_tensor(q.shape, dt, q.device, stream) if dq is None else dq
     dk = new_tensor(k.shape, dt, q.device, stream) if dk is None else dk
     dv = new_tensor(v.shape, dt, q.device, stream) if dv is None else dv
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _check_io(name, t, like.shape, dt)
     need = sdpa_bwd_varlen_workspace_size(b, h, total_q, d_qk, deterministic)
     if workspace is None:
         workspace = new_tensor(max(need, 1), torch.uint8, q.device, stream, scratch=True)
-    cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask)
+    ws = check_workspace(workspace, q.device)
+    words = _words(dropout_p, b, h, int(max_seqlen_q), int(max_seqlen_k))
+    cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask,
+                  words)
     if cap is not None:
         st = _native.lib().sdpa_bwd_phases_varlen_capped(
             int(phases), b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v,
             scale, *cap, float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q),
             _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
-            _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(), _stream_ptr(stream, q))
+            _ptr(dk), _ptr(dv), *ws, _stream_ptr(stream, q))
         _native.check(st, "sdpa_bwd_phases_varlen_capped")
         return dq, dk, dv
-    w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask)
+    w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask, words=words)
     if w is None:
         st = _native.lib().sdpa_bwd_phases_varlen(
             int(phases), b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk,
             d_v, scale, int(bool(is_causal)), float(dropout_p), int(seed), int(offset),
             _DTYPE_CODE[dt], _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(o),
-            _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
+            _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *ws,
             _stream_ptr(stream, q))
         _native.check(st, "sdpa_bwd_phases_varlen")
     else:
@@ -419,7 +449,7 @@ def sdpa_bwd_phases_varlen(phases, q, k, v, o, dout, lse, seqstart_q, seqstart_k
             int(phases), b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk,
             d_v, scale, *w, float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt],
             _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout),
-            _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
+            _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *ws,
             _stream_ptr(stream, q))
         _native.check(st, "sdpa_bwd_phases_varlen_ex")
     return dq, dk, dv
@@ -432,8 +462,9 @@ def sdpa_dropout_mask(b, h, s_q, s_kv, dropout_p, seed, offset, device="cuda", s
     read these bits instead of drawing them."""
     words = (b * h * s_q * s_kv + 31) // 32
     bits = new_tensor(max(words, 1), torch.int32, device, stream) if out is None else out
-    if out is not None and (out.dtype != torch.int32 or out.numel() < words or not out.is_cuda):
-        raise ValueError(f"out must be an int32 CUDA tensor of at least {words} words")
+    if out is not None and (out.dtype != torch.int32 or out.numel() < words or not out.is_cuda
+                            or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous int32 CUDA tensor of at least {words} words")
     st = _native.lib().sdpa_dropout_mask(b, h, s_q, s_kv, float(dropout_p), int(seed), int(offset),
                                          _ptr(bits), _stream_ptr(stream, bits))
     _native.check(st, "sdpa_dropout_mask")

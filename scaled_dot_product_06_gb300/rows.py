@@ -13,7 +13,7 @@ import struct
 import torch
 
 from . import _native
-from .api import _DTYPE_CODE, _ptr, _stream_ptr, new_tensor
+from .api import _DTYPE_CODE, _ptr, _stream_ptr, check_workspace, new_tensor
 
 _NO_GUARD = contextlib.nullcontext()
 _pack_rows = struct.Struct("Pqqq").pack  # the bytes of an sdpa_rows_t
@@ -224,13 +224,12 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos, sin, *, dv_out=None, positi
         grads.append(g)
     if workspace is None and (q_weight is not None or k_weight is not None):
         workspace = new_tensor(max(_bwd_bytes(b, s, h, h_kv, d, d_v), 1), torch.uint8, dev, stream, scratch=True)
+    ws = (None, 0) if workspace is None else check_workspace(workspace, dev)
     with on_device(q):
         st = _native.lib().sdpa_qk_norm_rope_bwd(
             b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], gq, gk, gv, q_in, k_in, q_to, k_to, v_to, rot,
             int(bool(interleaved)), cos_p, sin_p, n_pos, pos_p, qw_p, kw_p, fp32, eps, _ptr(grads[0]),
-            _ptr(grads[1]), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream_ptr(stream, q))
+            _ptr(grads[1]), *ws, _stream_ptr(stream, q))
     if st:
         _native.check(st, "sdpa_qk_norm_rope_bwd")
     return dq, dk, dv, grads[0], grads[1]
