@@ -12,6 +12,7 @@ keeping the inputs until it has run.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -39,6 +40,22 @@ def _stream_ptr(stream, t: torch.Tensor) -> int:
     return int(torch.cuda.current_stream(t.device).cuda_stream)
 
 
+_NO_GUARD = contextlib.nullcontext()
+
+
+def on_device(t: torch.Tensor):
+    """Makes t's device current for a launch where it is not already."""
+    return _NO_GUARD if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _run(t: torch.Tensor, name: str, *args) -> None:
+    """Calls the C entry point `name` with t's device current."""
+    with on_device(t):
+        st = getattr(_native.lib(), name)(*args)
+    if st:
+        _native.check(st, name)
+
+
 def new_tensor(shape, dtype, device, stream, scratch=False) -> torch.Tensor:
     """Memory for a call on ``stream`` (None: the current one).
 
@@ -59,16 +76,27 @@ def new_tensor(shape, dtype, device, stream, scratch=False) -> torch.Tensor:
     return t
 
 
-def _check_io(name: str, t: torch.Tensor, shape, dtype) -> None:
-    if t.is_cuda and t.shape == shape and t.dtype == dtype and t.is_contiguous():
+def _check_io(name: str, t: torch.Tensor, shape, dtype, device=None) -> None:
+    """A contiguous CUDA tensor of this shape and type (and device)."""
+    if (t.is_cuda if device is None else t.device == device) and t.shape == shape and t.dtype == dtype \
+            and t.is_contiguous():
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on the device of q")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     raise ValueError(f"{name} must be contiguous (BHSD)")
+
+
+def _check_device(device, **tensors) -> None:
+    """The smaller operands, whose form is checked elsewhere, are on q's device."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on the device of q")
 
 
 def check_workspace(t: torch.Tensor, device):
@@ -163,43 +191,39 @@ def sdpa_fwd(q, k, v, *, scale=None, is_causal=False, dropout_p=0.0, seed=0, off
     if dt not in _DTYPE_CODE:
         raise ValueError("q, k, v must be bf16 or fp16")
     _check_io("q", q, (b, h, s_q, d_qk), dt)
-    _check_io("k", k, (b, h_kv, s_kv, d_qk), dt)
-    _check_io("v", v, (b, h_kv, s_kv, d_v), dt)
+    _check_io("k", k, (b, h_kv, s_kv, d_qk), dt, q.device)
+    _check_io("v", v, (b, h_kv, s_kv, d_v), dt, q.device)
     if bias is not None:
-        _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32)
+        _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32, q.device)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
     if out is None:
         out = new_tensor((b, h, s_q, d_v), dt, q.device, stream)
     if lse is None:
         lse = new_tensor((b, h, s_q), torch.float32, q.device, stream)
-    _check_io("out", out, (b, h, s_q, d_v), dt)
-    _check_io("lse", lse, (b, h, s_q), torch.float32)
+    _check_io("out", out, (b, h, s_q, d_v), dt, q.device)
+    _check_io("lse", lse, (b, h, s_q), torch.float32, q.device)
+    _check_device(q.device, alibi_slopes=alibi_slopes,
+                  dropout_mask=dropout_mask, dropout_mask_out=dropout_mask_out)
     words = _words(dropout_p, b, h, s_q, s_kv)
     cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask,
                   words)
     if cap is not None:
         rec = _mask_out(dropout_mask_out, (b * h * s_q * s_kv + 31) // 32)
-        st = _native.lib().sdpa_fwd_capped(b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *cap, rec,
-                                           float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt],
-                                           _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                           _stream_ptr(stream, q))
-        _native.check(st, "sdpa_fwd_capped")
+        _run(q, "sdpa_fwd_capped", b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *cap, rec,
+             float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v),
+             _ptr(out), _ptr(lse), _stream_ptr(stream, q))
         return out, lse
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask,
                 force=dropout_mask_out is not None, words=words)
     if w is None:
-        st = _native.lib().sdpa_fwd_gqa(b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, int(bool(is_causal)),
-                                        float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt],
-                                        _ptr(q), _ptr(k), _ptr(v), _ptr(bias), _ptr(out), _ptr(lse),
-                                        _stream_ptr(stream, q))
-        _native.check(st, "sdpa_fwd_gqa")
+        _run(q, "sdpa_fwd_gqa", b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, int(bool(is_causal)),
+             float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v),
+             _ptr(bias), _ptr(out), _ptr(lse), _stream_ptr(stream, q))
     else:
         rec = _mask_out(dropout_mask_out, (b * h * s_q * s_kv + 31) // 32)
-        st = _native.lib().sdpa_fwd_ex(b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *w, rec,
-                                           float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt],
-                                           _ptr(q), _ptr(k), _ptr(v), _ptr(bias), _ptr(out),
-                                           _ptr(lse), _stream_ptr(stream, q))
-        _native.check(st, "sdpa_fwd_ex")
+        _run(q, "sdpa_fwd_ex", b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *w, rec, float(dropout_p),
+             int(seed), int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v), _ptr(bias),
+             _ptr(out), _ptr(lse), _stream_ptr(stream, q))
     return out, lse
 
 
@@ -251,49 +275,45 @@ def sdpa_bwd_phases(phases, q, k, v, o, dout, lse, *, scale=None, is_causal=Fals
     for name, t, shp in (("q", q, (b, h, s_q, d_qk)), ("k", k, (b, h_kv, s_kv, d_qk)),
                          ("v", v, (b, h_kv, s_kv, d_v)), ("o", o, (b, h, s_q, d_v)),
                          ("dout", dout, (b, h, s_q, d_v))):
-        _check_io(name, t, shp, dt)
-    _check_io("lse", lse, (b, h, s_q), torch.float32)
+        _check_io(name, t, shp, dt, q.device if t is not q else None)
+    _check_io("lse", lse, (b, h, s_q), torch.float32, q.device)
     if bias is not None:
-        _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32)
+        _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32, q.device)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
     dq = new_tensor(q.shape, dt, q.device, stream) if dq is None else dq
     dk = new_tensor(k.shape, dt, q.device, stream) if dk is None else dk
     dv = new_tensor(v.shape, dt, q.device, stream) if dv is None else dv
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _check_io(name, t, like.shape, dt)
+        _check_io(name, t, like.shape, dt, q.device)
     if bias is not None and dbias is None:
         dbias = new_tensor(bias.shape, torch.float32, q.device, stream)
     if dbias is not None:
-        _check_io("dbias", dbias, (1, h, s_q, s_kv), torch.float32)
+        _check_io("dbias", dbias, (1, h, s_q, s_kv), torch.float32, q.device)
     need = sdpa_bwd_workspace_size(b, h, s_q, s_kv, d_qk, d_v, h_kv, deterministic)
     if workspace is None:
         workspace = new_tensor(max(need, 1), torch.uint8, q.device, stream, scratch=True)
     ws = check_workspace(workspace, q.device)
+    _check_device(q.device, alibi_slopes=alibi_slopes, dropout_mask=dropout_mask)
     words = _words(dropout_p, b, h, s_q, s_kv)
     cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask,
                   words)
     if cap is not None:
-        st = _native.lib().sdpa_bwd_phases_capped(
-            int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *cap, float(dropout_p), int(seed),
-            int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
-            _ptr(dq), _ptr(dk), _ptr(dv), *ws, _stream_ptr(stream, q))
-        _native.check(st, "sdpa_bwd_phases_capped")
+        _run(q, "sdpa_bwd_phases_capped", int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale,
+             *cap, float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k),
+             _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *ws,
+             _stream_ptr(stream, q))
         return dq, dk, dv, None
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask, words=words)
     if w is None:
-        st = _native.lib().sdpa_bwd_phases_gqa(
-            int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, int(bool(is_causal)),
-            float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v),
-            _ptr(bias), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias),
-            *ws, _stream_ptr(stream, q))
-        _native.check(st, "sdpa_bwd_phases_gqa")
+        _run(q, "sdpa_bwd_phases_gqa", int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale,
+             int(bool(is_causal)), float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt],
+             _ptr(q), _ptr(k), _ptr(v), _ptr(bias), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
+             _ptr(dk), _ptr(dv), _ptr(dbias), *ws, _stream_ptr(stream, q))
     else:
-        st = _native.lib().sdpa_bwd_phases_ex(
-            int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *w, float(dropout_p), int(seed),
-            int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v), _ptr(bias), _ptr(o),
-            _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias), *ws,
-            _stream_ptr(stream, q))
-        _native.check(st, "sdpa_bwd_phases_ex")
+        _run(q, "sdpa_bwd_phases_ex", int(phases), b, h, h_kv, s_q, s_kv, d_qk, d_v, scale, *w,
+             float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(q), _ptr(k), _ptr(v),
+             _ptr(bias), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias),
+             *ws, _stream_ptr(stream, q))
     return dq, dk, dv, dbias
 
 
@@ -323,43 +343,40 @@ def sdpa_fwd_varlen(q, k, v, seqstart_q, seqstart_k, max_seqlen_q, max_seqlen_k,
     if _check_seqstart("seqstart_k", seqstart_k) != b:
         raise ValueError("seqstart_q and seqstart_k must have the same length")
     _check_io("q", q, (h, total_q, d_qk), dt)
-    _check_io("k", k, (h_kv, total_k, d_qk), dt)
-    _check_io("v", v, (h_kv, total_k, d_v), dt)
+    _check_io("k", k, (h_kv, total_k, d_qk), dt, q.device)
+    _check_io("v", v, (h_kv, total_k, d_v), dt, q.device)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
     if out is None:
         out = new_tensor((h, total_q, d_v), dt, q.device, stream)
     if lse is None:
         lse = new_tensor((h, total_q), torch.float32, q.device, stream)
-    _check_io("out", out, (h, total_q, d_v), dt)
-    _check_io("lse", lse, (h, total_q), torch.float32)
+    _check_io("out", out, (h, total_q, d_v), dt, q.device)
+    _check_io("lse", lse, (h, total_q), torch.float32, q.device)
+    _check_device(q.device, seqstart_q=seqstart_q, seqstart_k=seqstart_k,
+                  alibi_slopes=alibi_slopes, dropout_mask=dropout_mask, dropout_mask_out=dropout_mask_out)
     words = _words(dropout_p, b, h, int(max_seqlen_q), int(max_seqlen_k))
     cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask,
                   words)
     if cap is not None:
         rec = _mask_out(dropout_mask_out, (b * h * int(max_seqlen_q) * int(max_seqlen_k) + 31) // 32)
-        st = _native.lib().sdpa_fwd_varlen_capped(
-            b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v, scale, *cap,
-            rec, float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q),
-            _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _stream_ptr(stream, q))
-        _native.check(st, "sdpa_fwd_varlen_capped")
+        _run(q, "sdpa_fwd_varlen_capped", b, h, h_kv, total_q, total_k, int(max_seqlen_q),
+             int(max_seqlen_k), d_qk, d_v, scale, *cap, rec, float(dropout_p), int(seed),
+             int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q), _ptr(k),
+             _ptr(v), _ptr(out), _ptr(lse), _stream_ptr(stream, q))
         return out, lse
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask,
                 force=dropout_mask_out is not None, words=words)
     if w is None:
-        st = _native.lib().sdpa_fwd_varlen(
-            b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v, scale,
-            int(bool(is_causal)), float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt],
-            _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-            _stream_ptr(stream, q))
-        _native.check(st, "sdpa_fwd_varlen")
+        _run(q, "sdpa_fwd_varlen", b, h, h_kv, total_q, total_k, int(max_seqlen_q),
+             int(max_seqlen_k), d_qk, d_v, scale, int(bool(is_causal)), float(dropout_p), int(seed),
+             int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q), _ptr(k),
+             _ptr(v), _ptr(out), _ptr(lse), _stream_ptr(stream, q))
     else:
         rec = _mask_out(dropout_mask_out, (b * h * int(max_seqlen_q) * int(max_seqlen_k) + 31) // 32)
-        st = _native.lib().sdpa_fwd_varlen_ex(
-            b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v, scale, *w,
-            rec, float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q),
-            _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-            _stream_ptr(stream, q))
-        _native.check(st, "sdpa_fwd_varlen_ex")
+        _run(q, "sdpa_fwd_varlen_ex", b, h, h_kv, total_q, total_k, int(max_seqlen_q),
+             int(max_seqlen_k), d_qk, d_v, scale, *w, rec, float(dropout_p), int(seed), int(offset),
+             _DTYPE_CODE[dt], _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v),
+             _ptr(out), _ptr(lse), _stream_ptr(stream, q))
     return out, lse
 
 
@@ -412,46 +429,43 @@ def sdpa_bwd_phases_varlen(phases, q, k, v, o, dout, lse, seqstart_q, seqstart_k
     for name, t, shp in (("q", q, (h, total_q, d_qk)), ("k", k, (h_kv, total_k, d_qk)),
                          ("v", v, (h_kv, total_k, d_v)), ("o", o, (h, total_q, d_v)),
                          ("dout", dout, (h, total_q, d_v))):
-        _check_io(name, t, shp, dt)
-    _check_io("lse", lse, (h, total_q), torch.float32)
+        _check_io(name, t, shp, dt, q.device if t is not q else None)
+    _check_io("lse", lse, (h, total_q), torch.float32, q.device)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
     dq = new_tensor(q.shape, dt, q.device, stream) if dq is None else dq
     dk = new_tensor(k.shape, dt, q.device, stream) if dk is None else dk
     dv = new_tensor(v.shape, dt, q.device, stream) if dv is None else dv
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _check_io(name, t, like.shape, dt)
+        _check_io(name, t, like.shape, dt, q.device)
     need = sdpa_bwd_varlen_workspace_size(b, h, total_q, d_qk, deterministic)
     if workspace is None:
         workspace = new_tensor(max(need, 1), torch.uint8, q.device, stream, scratch=True)
     ws = check_workspace(workspace, q.device)
+    _check_device(q.device, seqstart_q=seqstart_q, seqstart_k=seqstart_k,
+                  alibi_slopes=alibi_slopes, dropout_mask=dropout_mask)
     words = _words(dropout_p, b, h, int(max_seqlen_q), int(max_seqlen_k))
     cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask,
                   words)
     if cap is not None:
-        st = _native.lib().sdpa_bwd_phases_varlen_capped(
-            int(phases), b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v,
-            scale, *cap, float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q),
-            _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
-            _ptr(dk), _ptr(dv), *ws, _stream_ptr(stream, q))
-        _native.check(st, "sdpa_bwd_phases_varlen_capped")
+        _run(q, "sdpa_bwd_phases_varlen_capped", int(phases), b, h, h_kv, total_q, total_k,
+             int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v, scale, *cap, float(dropout_p),
+             int(seed), int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q),
+             _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *ws,
+             _stream_ptr(stream, q))
         return dq, dk, dv
     w = _window(is_causal, window, bottom_right, alibi_slopes, b, h, dropout_mask, words=words)
     if w is None:
-        st = _native.lib().sdpa_bwd_phases_varlen(
-            int(phases), b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk,
-            d_v, scale, int(bool(is_causal)), float(dropout_p), int(seed), int(offset),
-            _DTYPE_CODE[dt], _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(o),
-            _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *ws,
-            _stream_ptr(stream, q))
-        _native.check(st, "sdpa_bwd_phases_varlen")
+        _run(q, "sdpa_bwd_phases_varlen", int(phases), b, h, h_kv, total_q, total_k,
+             int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v, scale, int(bool(is_causal)),
+             float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q),
+             _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
+             _ptr(dk), _ptr(dv), *ws, _stream_ptr(stream, q))
     else:
-        st = _native.lib().sdpa_bwd_phases_varlen_ex(
-            int(phases), b, h, h_kv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d_qk,
-            d_v, scale, *w, float(dropout_p), int(seed), int(offset), _DTYPE_CODE[dt],
-            _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout),
-            _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *ws,
-            _stream_ptr(stream, q))
-        _native.check(st, "sdpa_bwd_phases_varlen_ex")
+        _run(q, "sdpa_bwd_phases_varlen_ex", int(phases), b, h, h_kv, total_q, total_k,
+             int(max_seqlen_q), int(max_seqlen_k), d_qk, d_v, scale, *w, float(dropout_p),
+             int(seed), int(offset), _DTYPE_CODE[dt], _ptr(seqstart_q), _ptr(seqstart_k), _ptr(q),
+             _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *ws,
+             _stream_ptr(stream, q))
     return dq, dk, dv
 
 
@@ -465,9 +479,8 @@ def sdpa_dropout_mask(b, h, s_q, s_kv, dropout_p, seed, offset, device="cuda", s
     if out is not None and (out.dtype != torch.int32 or out.numel() < words or not out.is_cuda
                             or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous int32 CUDA tensor of at least {words} words")
-    st = _native.lib().sdpa_dropout_mask(b, h, s_q, s_kv, float(dropout_p), int(seed), int(offset),
-                                         _ptr(bits), _stream_ptr(stream, bits))
-    _native.check(st, "sdpa_dropout_mask")
+    _run(bits, "sdpa_dropout_mask", b, h, s_q, s_kv, float(dropout_p), int(seed), int(offset), _ptr(bits),
+         _stream_ptr(stream, bits))
     return bits[:words]
 
 

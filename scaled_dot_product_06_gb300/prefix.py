@@ -7,8 +7,8 @@ import math
 import torch
 
 from . import _native
-from .api import _DTYPE_CODE, _stream_ptr, check_workspace, new_tensor
-from .rows import check_flat, on_device
+from .api import _DTYPE_CODE, _run, _stream_ptr, check_workspace, new_tensor
+from .rows import check_flat
 
 
 @functools.lru_cache(maxsize=256)
@@ -60,11 +60,7 @@ def sdpa_fwd_prefix(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, softc
         workspace = new_tensor(max(_bytes(b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v), 1), torch.uint8, dev,
                                stream, scratch=True)
     ws = check_workspace(workspace, dev)
-    with on_device(q):
-        st = _native.lib().sdpa_fwd_prefix(
-            b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v, 1.0 / math.sqrt(d_qk) if scale is None else scale,
-            softcap or 0.0, _DTYPE_CODE[dt], q_p, kp_p, vp_p, k_p, v_p, n_p, o_p, l_p,
-            *ws, _stream_ptr(stream, q))
-    if st:
-        _native.check(st, "sdpa_fwd_prefix")
+    _run(q, "sdpa_fwd_prefix", b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v,
+         1.0 / math.sqrt(d_qk) if scale is None else scale, softcap or 0.0, _DTYPE_CODE[dt], q_p, kp_p, vp_p,
+         k_p, v_p, n_p, o_p, l_p, *ws, _stream_ptr(stream, q))
     return out, lse

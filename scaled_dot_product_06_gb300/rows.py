@@ -6,22 +6,15 @@ torch and pass pointers and strides; all arithmetic is in libsdpa.so.
 """
 from __future__ import annotations
 
-import contextlib
 import functools
 import struct
 
 import torch
 
 from . import _native
-from .api import _DTYPE_CODE, _ptr, _stream_ptr, check_workspace, new_tensor
+from .api import _DTYPE_CODE, _ptr, _run, _stream_ptr, check_workspace, new_tensor
 
-_NO_GUARD = contextlib.nullcontext()
 _pack_rows = struct.Struct("Pqqq").pack  # the bytes of an sdpa_rows_t
-
-
-def on_device(t: torch.Tensor):
-    """Makes t's device current for a launch where it is not already."""
-    return _NO_GUARD if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 def check_rows(name, t, shape, dtype, device):
@@ -156,13 +149,9 @@ def sdpa_qk_norm_rope(q, k, cos, sin, *, v=None, positions=None, q_weight=None, 
         else:
             _check_output("v_out", v_out)
         v_to = _head_rows("v_out", v_out, (b, h_kv, cache, d_v), dt, dev)
-    with on_device(q):
-        st = _native.lib().sdpa_qk_norm_rope(
-            b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], q_in, k_in, v_in, q_to, k_to, v_to, rot,
-            int(bool(interleaved)), cos_p, sin_p, n_pos, pos_p, qw_p, kw_p, fp32, eps, rows_p, cache,
-            _stream_ptr(stream, q))
-    if st:
-        _native.check(st, "sdpa_qk_norm_rope")
+    _run(q, "sdpa_qk_norm_rope", b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], q_in, k_in, v_in, q_to, k_to, v_to,
+         rot, int(bool(interleaved)), cos_p, sin_p, n_pos, pos_p, qw_p, kw_p, fp32, eps, rows_p, cache,
+         _stream_ptr(stream, q))
     return q_out, k_out, v_out
 
 
@@ -225,11 +214,7 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos, sin, *, dv_out=None, positi
     if workspace is None and (q_weight is not None or k_weight is not None):
         workspace = new_tensor(max(_bwd_bytes(b, s, h, h_kv, d, d_v), 1), torch.uint8, dev, stream, scratch=True)
     ws = (None, 0) if workspace is None else check_workspace(workspace, dev)
-    with on_device(q):
-        st = _native.lib().sdpa_qk_norm_rope_bwd(
-            b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], gq, gk, gv, q_in, k_in, q_to, k_to, v_to, rot,
-            int(bool(interleaved)), cos_p, sin_p, n_pos, pos_p, qw_p, kw_p, fp32, eps, _ptr(grads[0]),
-            _ptr(grads[1]), *ws, _stream_ptr(stream, q))
-    if st:
-        _native.check(st, "sdpa_qk_norm_rope_bwd")
+    _run(q, "sdpa_qk_norm_rope_bwd", b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], gq, gk, gv, q_in, k_in, q_to,
+         k_to, v_to, rot, int(bool(interleaved)), cos_p, sin_p, n_pos, pos_p, qw_p, kw_p, fp32, eps,
+         _ptr(grads[0]), _ptr(grads[1]), *ws, _stream_ptr(stream, q))
     return dq, dk, dv, grads[0], grads[1]
