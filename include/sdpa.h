@@ -469,8 +469,9 @@ sdpa_status_t sdpa_bwd_phases_varlen_capped(
  * and the forward's inputs q, k (null where there is no weight), and writes
  * dq, dk, dv in the projection's layout (any strides) and dq_weight,
  * dk_weight ([d], the weights' type; null where there is no weight), summed
- * over all rows in fp32 in an order that depends on the sizes alone, so they
- * are reproducible bit for bit. dq, dk may be the storage of dq_out, dk_out
+ * over all rows in fp32 in an order that depends on the sizes and on which of
+ * values and weights there are, and on nothing else: the same call gives the
+ * same bits in every run. dq, dk may be the storage of dq_out, dk_out
  * in no case. Workspace: 256-byte aligned, of the size given, with a weight.
  * b or s of 0: a no-op (the weight gradients become 0).
  */

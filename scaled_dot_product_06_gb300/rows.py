@@ -172,8 +172,9 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos, sin, *, dv_out=None, positi
     dk_out [b, h_kv, s, d] and optionally dv_out are the gradients of its
     outputs, q and k its inputs. Returns (dq [b, s, h, d], dk, dv or None,
     dq_weight or None, dk_weight or None); dq, dk, dv may be given as slices of
-    one fused gradient. The weight gradients have the weights' dtype and the
-    same bits in every run."""
+    one fused gradient. The weight gradients have the weights' dtype and, for
+    the same call, the same bits in every run (their sums' order depends on the
+    sizes and on which of values and weights there are)."""
     _check_qkv(q, k, None)
     if dq_out.dim() != 4 or dk_out.dim() != 4 or (dv_out is not None and dv_out.dim() != 4):
         raise ValueError("dq_out, dk_out and dv_out must have 4 dimensions")
