@@ -12,7 +12,6 @@ keeping the inputs until it has run.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -40,18 +39,13 @@ def _stream_ptr(stream, t: torch.Tensor) -> int:
     return int(torch.cuda.current_stream(t.device).cuda_stream)
 
 
-_NO_GUARD = contextlib.nullcontext()
-
-
-def on_device(t: torch.Tensor):
-    """Makes t's device current for a launch where it is not already."""
-    return _NO_GUARD if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-
 def _run(t: torch.Tensor, name: str, *args) -> None:
     """Calls the C entry point `name` with t's device current."""
-    with on_device(t):
+    if t.get_device() == torch.cuda.current_device():
         st = getattr(_native.lib(), name)(*args)
+    else:
+        with torch.cuda.device(t.device):
+            st = getattr(_native.lib(), name)(*args)
     if st:
         _native.check(st, name)
 
@@ -104,6 +98,14 @@ def check_workspace(t: torch.Tensor, device):
     if t.device != device or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the device of q")
     return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _grad(name, t, shape, dtype, device, stream) -> torch.Tensor:
+    """A gradient: the given tensor, checked, or a new one."""
+    if t is None:
+        return new_tensor(shape, dtype, device, stream)
+    _check_io(name, t, shape, dtype, device)
+    return t
 
 
 def _ptr(t):
@@ -187,23 +189,26 @@ def sdpa_fwd(q, k, v, *, scale=None, is_causal=False, dropout_p=0.0, seed=0, off
     softcap * tanh(s / softcap) before the mask; not with a bias or ALiBi."""
     b, h, s_q, d_qk = q.shape
     h_kv, s_kv, d_v = k.shape[1], k.shape[2], v.shape[3]
-    dt = q.dtype
+    dt, dev = q.dtype, q.device
     if dt not in _DTYPE_CODE:
         raise ValueError("q, k, v must be bf16 or fp16")
     _check_io("q", q, (b, h, s_q, d_qk), dt)
-    _check_io("k", k, (b, h_kv, s_kv, d_qk), dt, q.device)
-    _check_io("v", v, (b, h_kv, s_kv, d_v), dt, q.device)
+    _check_io("k", k, (b, h_kv, s_kv, d_qk), dt, dev)
+    _check_io("v", v, (b, h_kv, s_kv, d_v), dt, dev)
     if bias is not None:
-        _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32, q.device)
+        _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32, dev)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
     if out is None:
-        out = new_tensor((b, h, s_q, d_v), dt, q.device, stream)
+        out = new_tensor((b, h, s_q, d_v), dt, dev, stream)
+    else:
+        _check_io("out", out, (b, h, s_q, d_v), dt, dev)
     if lse is None:
-        lse = new_tensor((b, h, s_q), torch.float32, q.device, stream)
-    _check_io("out", out, (b, h, s_q, d_v), dt, q.device)
-    _check_io("lse", lse, (b, h, s_q), torch.float32, q.device)
-    _check_device(q.device, alibi_slopes=alibi_slopes,
-                  dropout_mask=dropout_mask, dropout_mask_out=dropout_mask_out)
+        lse = new_tensor((b, h, s_q), torch.float32, dev, stream)
+    else:
+        _check_io("lse", lse, (b, h, s_q), torch.float32, dev)
+    if alibi_slopes is not None or dropout_p > 0:
+        _check_device(dev, alibi_slopes=alibi_slopes, dropout_mask=dropout_mask,
+                      dropout_mask_out=dropout_mask_out)
     words = _words(dropout_p, b, h, s_q, s_kv)
     cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask,
                   words)
@@ -269,31 +274,30 @@ def sdpa_bwd_phases(phases, q, k, v, o, dout, lse, *, scale=None, is_causal=Fals
     phases = int(phases) | (_native.SDPA_BWD_DETERMINISTIC if deterministic else 0)
     b, h, s_q, d_qk = q.shape
     h_kv, s_kv, d_v = k.shape[1], k.shape[2], v.shape[3]
-    dt = q.dtype
+    dt, dev = q.dtype, q.device
     if dt not in _DTYPE_CODE:
         raise ValueError("q, k, v must be bf16 or fp16")
     for name, t, shp in (("q", q, (b, h, s_q, d_qk)), ("k", k, (b, h_kv, s_kv, d_qk)),
                          ("v", v, (b, h_kv, s_kv, d_v)), ("o", o, (b, h, s_q, d_v)),
                          ("dout", dout, (b, h, s_q, d_v))):
-        _check_io(name, t, shp, dt, q.device if t is not q else None)
-    _check_io("lse", lse, (b, h, s_q), torch.float32, q.device)
+        _check_io(name, t, shp, dt, dev if t is not q else None)
+    _check_io("lse", lse, (b, h, s_q), torch.float32, dev)
     if bias is not None:
-        _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32, q.device)
+        _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32, dev)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
-    dq = new_tensor(q.shape, dt, q.device, stream) if dq is None else dq
-    dk = new_tensor(k.shape, dt, q.device, stream) if dk is None else dk
-    dv = new_tensor(v.shape, dt, q.device, stream) if dv is None else dv
-    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _check_io(name, t, like.shape, dt, q.device)
-    if bias is not None and dbias is None:
-        dbias = new_tensor(bias.shape, torch.float32, q.device, stream)
-    if dbias is not None:
-        _check_io("dbias", dbias, (1, h, s_q, s_kv), torch.float32, q.device)
+    dq = _grad("dq", dq, q.shape, dt, dev, stream)
+    dk = _grad("dk", dk, k.shape, dt, dev, stream)
+    dv = _grad("dv", dv, v.shape, dt, dev, stream)
+    if bias is not None or dbias is not None:
+        dbias = _grad("dbias", dbias, (1, h, s_q, s_kv), torch.float32, dev, stream)
     need = sdpa_bwd_workspace_size(b, h, s_q, s_kv, d_qk, d_v, h_kv, deterministic)
     if workspace is None:
-        workspace = new_tensor(max(need, 1), torch.uint8, q.device, stream, scratch=True)
-    ws = check_workspace(workspace, q.device)
-    _check_device(q.device, alibi_slopes=alibi_slopes, dropout_mask=dropout_mask)
+        workspace = new_tensor(max(need, 1), torch.uint8, dev, stream, scratch=True)
+        ws = workspace.data_ptr(), need
+    else:
+        ws = check_workspace(workspace, dev)
+    if alibi_slopes is not None or dropout_p > 0:
+        _check_device(dev, alibi_slopes=alibi_slopes, dropout_mask=dropout_mask)
     words = _words(dropout_p, b, h, s_q, s_kv)
     cap = _capped(softcap, is_causal, window, bottom_right, bias, alibi_slopes, b, h, dropout_mask,
                   words)
@@ -336,24 +340,26 @@ def sdpa_fwd_varlen(q, k, v, seqstart_q, seqstart_k, max_seqlen_q, max_seqlen_k,
     Returns (o [h, total_q, d_v], lse fp32 [h, total_q])."""
     h, total_q, d_qk = q.shape
     h_kv, total_k, d_v = k.shape[0], k.shape[1], v.shape[2]
-    dt = q.dtype
+    dt, dev = q.dtype, q.device
     if dt not in _DTYPE_CODE:
         raise ValueError("q, k, v must be bf16 or fp16")
     b = _check_seqstart("seqstart_q", seqstart_q)
     if _check_seqstart("seqstart_k", seqstart_k) != b:
         raise ValueError("seqstart_q and seqstart_k must have the same length")
     _check_io("q", q, (h, total_q, d_qk), dt)
-    _check_io("k", k, (h_kv, total_k, d_qk), dt, q.device)
-    _check_io("v", v, (h_kv, total_k, d_v), dt, q.device)
+    _check_io("k", k, (h_kv, total_k, d_qk), dt, dev)
+    _check_io("v", v, (h_kv, total_k, d_v), dt, dev)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
     if out is None:
-        out = new_tensor((h, total_q, d_v), dt, q.device, stream)
+        out = new_tensor((h, total_q, d_v), dt, dev, stream)
+    else:
+        _check_io("out", out, (h, total_q, d_v), dt, dev)
     if lse is None:
-        lse = new_tensor((h, total_q), torch.float32, q.device, stream)
-    _check_io("out", out, (h, total_q, d_v), dt, q.device)
-    _check_io("lse", lse, (h, total_q), torch.float32, q.device)
-    _check_device(q.device, seqstart_q=seqstart_q, seqstart_k=seqstart_k,
-                  alibi_slopes=alibi_slopes, dropout_mask=dropout_mask, dropout_mask_out=dropout_mask_out)
+        lse = new_tensor((h, total_q), torch.float32, dev, stream)
+    else:
+        _check_io("lse", lse, (h, total_q), torch.float32, dev)
+    _check_device(dev, seqstart_q=seqstart_q, seqstart_k=seqstart_k, alibi_slopes=alibi_slopes,
+                  dropout_mask=dropout_mask, dropout_mask_out=dropout_mask_out)
     words = _words(dropout_p, b, h, int(max_seqlen_q), int(max_seqlen_k))
     cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask,
                   words)
@@ -420,7 +426,7 @@ def sdpa_bwd_phases_varlen(phases, q, k, v, o, dout, lse, seqstart_q, seqstart_k
     phases = int(phases) | (_native.SDPA_BWD_DETERMINISTIC if deterministic else 0)
     h, total_q, d_qk = q.shape
     h_kv, total_k, d_v = k.shape[0], k.shape[1], v.shape[2]
-    dt = q.dtype
+    dt, dev = q.dtype, q.device
     if dt not in _DTYPE_CODE:
         raise ValueError("q, k, v must be bf16 or fp16")
     b = _check_seqstart("seqstart_q", seqstart_q)
@@ -429,20 +435,20 @@ def sdpa_bwd_phases_varlen(phases, q, k, v, o, dout, lse, seqstart_q, seqstart_k
     for name, t, shp in (("q", q, (h, total_q, d_qk)), ("k", k, (h_kv, total_k, d_qk)),
                          ("v", v, (h_kv, total_k, d_v)), ("o", o, (h, total_q, d_v)),
                          ("dout", dout, (h, total_q, d_v))):
-        _check_io(name, t, shp, dt, q.device if t is not q else None)
-    _check_io("lse", lse, (h, total_q), torch.float32, q.device)
+        _check_io(name, t, shp, dt, dev if t is not q else None)
+    _check_io("lse", lse, (h, total_q), torch.float32, dev)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
-    dq = new_tensor(q.shape, dt, q.device, stream) if dq is None else dq
-    dk = new_tensor(k.shape, dt, q.device, stream) if dk is None else dk
-    dv = new_tensor(v.shape, dt, q.device, stream) if dv is None else dv
-    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _check_io(name, t, like.shape, dt, q.device)
+    dq = _grad("dq", dq, q.shape, dt, dev, stream)
+    dk = _grad("dk", dk, k.shape, dt, dev, stream)
+    dv = _grad("dv", dv, v.shape, dt, dev, stream)
     need = sdpa_bwd_varlen_workspace_size(b, h, total_q, d_qk, deterministic)
     if workspace is None:
-        workspace = new_tensor(max(need, 1), torch.uint8, q.device, stream, scratch=True)
-    ws = check_workspace(workspace, q.device)
-    _check_device(q.device, seqstart_q=seqstart_q, seqstart_k=seqstart_k,
-                  alibi_slopes=alibi_slopes, dropout_mask=dropout_mask)
+        workspace = new_tensor(max(need, 1), torch.uint8, dev, stream, scratch=True)
+        ws = workspace.data_ptr(), need
+    else:
+        ws = check_workspace(workspace, dev)
+    _check_device(dev, seqstart_q=seqstart_q, seqstart_k=seqstart_k, alibi_slopes=alibi_slopes,
+                  dropout_mask=dropout_mask)
     words = _words(dropout_p, b, h, int(max_seqlen_q), int(max_seqlen_k))
     cap = _capped(softcap, is_causal, window, bottom_right, None, alibi_slopes, b, h, dropout_mask,
                   words)

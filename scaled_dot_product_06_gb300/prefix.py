@@ -57,9 +57,11 @@ def sdpa_fwd_prefix(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, softc
     o_p = check_flat("out", out, (b, h, s_q, d_v), dt, dev)
     l_p = check_flat("lse", lse, (b, h, s_q), torch.float32, dev)
     if workspace is None:
-        workspace = new_tensor(max(_bytes(b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v), 1), torch.uint8, dev,
-                               stream, scratch=True)
-    ws = check_workspace(workspace, dev)
+        need = _bytes(b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v)
+        workspace = new_tensor(max(need, 1), torch.uint8, dev, stream, scratch=True)
+        ws = workspace.data_ptr(), need
+    else:
+        ws = check_workspace(workspace, dev)
     _run(q, "sdpa_fwd_prefix", b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v,
          1.0 / math.sqrt(d_qk) if scale is None else scale, softcap or 0.0, _DTYPE_CODE[dt], q_p, kp_p, vp_p,
          k_p, v_p, n_p, o_p, l_p, *ws, _stream_ptr(stream, q))
