@@ -18,13 +18,14 @@
 // tells it to the other roles through a ring in shared memory. Which CTA has an
 // item does not change its result.
 //
-// Measured (b64 h32 kv4 d128 bf16 behind 16384 keys, own lengths up to 1024):
-// 36 us, and 7 us the join, for 14 us of bytes and 9 us of products: the start
-// (5 us), filling and emptying the pipeline at each item's ends (about 2 us) and
-// the items' grain are the rest. Own keys alone, 152 sequences of 4096: 5.7 TB/s;
-// a prefix of 131072 for 512 rows a K/V head: 1.4 PFLOP/s. Equal runs of visits
-// for each CTA instead of items (a stream cut at any tile, more partials, every
-// row block's borders found by a scan of the lengths) took 51 us there.
+// Measured (b64 h32 kv4 d128 bf16 behind 16384 keys, own lengths up to 1024, cap
+// 50): 50 us, and 6.4 us the join, for 17 us of bytes and 9 us of products: the
+// start (5 us), filling and emptying the pipeline at each item's ends (about 2 us)
+// and the items' grain are the rest. Whole calls without a cap: own keys alone, 152
+// sequences of 4096 keys, 61 us (5.2 TB/s); a prefix of 131072 for 512 rows of each
+// of 4 K/V heads, 105 us (1.3 PFLOP/s). Equal runs of visits for each CTA instead of
+// items (a stream cut at any tile, more partials, every row block's borders found by
+// a scan of the lengths) took 51 us where the first form of this kernel took 41.
 //
 // One persistent CTA an SM, two softmax warpgroups, one MMA issuer, one TMA
 // producer, as in the forward (fwd_kernel.cuh). An item runs in one of two
@@ -39,7 +40,9 @@
 //           32 rows go a step further (quart): Q lies four times in its tile, once
 //           for each warp's lanes, and a warp takes a quarter of a tile's keys, P
 //           of the others being 0: a warp alone with 128 columns of 8 rows would
-//           be what the stream waits for. Each warp leaves a partial.
+//           be what the stream waits for. Each warp leaves a partial. (64
+//           sequences of 512 own keys, 4 K/V heads: 21.1 us for 22.5 at 8 rows, 28.0
+//           for 26.0 at 32 rows; with a cap 22.2 for 27.0, and 29.0 for 30.4.)
 // MMA order per round: O_0 += P_0 V, S_0 of the next round, then the same for
 // warpgroup 1.
 #pragma once
@@ -416,20 +419,23 @@ __global__ void __launch_bounds__(384, 1)
         constexpr int N = decltype(width)::value;
         k0 += col;
         float xs[N];
+        if constexpr (CAP) {
+          // Eight scores of a row share their reciprocals: what lies behind the last key
+          // must not lend its roundings to those before it. Zeroed in tensor memory, by a
+          // loop: the unrolled softmaxes already miss the instruction cache.
+          const int behind = it.keys - k0;
+          if (behind > 0 && behind < N) {
+#pragma unroll 1
+            for (int c = behind; c & 7; ++c) tmem_st1(tS + lane_off + col + c, 0u);
+            tmem_wait_st();
+          }
+        }
 #pragma unroll
         for (int q = 0; q < N / 32; ++q) tmem_ld32f(tS + lane_off + col + q * 32, xs + q * 32);
         tmem_wait_ld();
         float mx = SDPA_NEG_INF;
         const bool hidden = k0 + N - 1 > all_see;  // there are hidden keys
-        if constexpr (CAP) {
-          // scores share reciprocals: what lies behind the last key must not lend its roundings
-          if (k0 + N > it.keys) {
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-              if (k0 + e >= it.keys) xs[e] = 0.f;
-          }
-          mx = cap_scores<N>(xs, p.cap_in, sl2, row_ok);
-        }
+        if constexpr (CAP) mx = cap_scores<N>(xs, p.cap_in, sl2, row_ok);
         if (hidden) {
 #pragma unroll
           for (int e = 0; e < N; ++e)

@@ -52,10 +52,14 @@ def sdpa_fwd_prefix(q, k_prefix, v_prefix, k, v, seqlens_k, *, scale=None, softc
     n_p = check_flat("seqlens_k", seqlens_k, (b,), torch.int32, dev)
     if out is None:
         out = new_tensor((b, h, s_q, d_v), dt, dev, stream)
+        o_p = out.data_ptr()
+    else:
+        o_p = check_flat("out", out, (b, h, s_q, d_v), dt, dev)
     if lse is None:
         lse = new_tensor((b, h, s_q), torch.float32, dev, stream)
-    o_p = check_flat("out", out, (b, h, s_q, d_v), dt, dev)
-    l_p = check_flat("lse", lse, (b, h, s_q), torch.float32, dev)
+        l_p = lse.data_ptr()
+    else:
+        l_p = check_flat("lse", lse, (b, h, s_q), torch.float32, dev)
     if workspace is None:
         need = _bytes(b, h, h_kv, s_q, s_prefix, s_max, d_qk, d_v)
         workspace = new_tensor(max(need, 1), torch.uint8, dev, stream, scratch=True)
