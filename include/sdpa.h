@@ -528,6 +528,9 @@ sdpa_status_t sdpa_qk_norm_rope_bwd(int64_t b, int64_t s, int64_t h, int64_t h_k
  *            one call to the next. Two calls that may run at the same time need
  *            one each.
  * Results are the same bits in every run. b, h or s_q of 0: a no-op.
+ * The work is cut by s_max, not by the lengths, which the host does not see: a
+ * cache far longer than what it holds costs time (4096 keys of one sequence, h 32,
+ * h_kv 8: 13.5 us with s_max 4096, 23.4 us with 131072).
  */
 size_t sdpa_fwd_prefix_workspace_size(int64_t b, int64_t h, int64_t h_kv, int64_t s_q,
                                       int64_t s_prefix, int64_t s_max, int64_t d_qk, int64_t d_v);

@@ -808,11 +808,14 @@ sdpa_status_t plan_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64
   const int64_t kt_p = (s_prefix + 127) / 128, kt_o = (s_max + 127) / 128;
   const int64_t items_p = blocks_p * h_kv, items_o = blocks_o * b * h_kv;
   // Key ranges of the items. A CTA's share of the key tiles, the own keys taken
-  // at half of their longest: items of 0.7 of it, but at least 4 tiles of the prefix and
-  // 8 own ones (an item costs about two of either besides), and no more of the
-  // prefix than CTAs; each range of a key set as long as the others. Items are handed out as CTAs ask for them, the
-  // prefix's long ones first. (Dealt out in turn, b64 h32 kv4 d128 behind 16384
-  // keys with own lengths up to 1024 took 47 us.)
+  // at half of the cache (their lengths are known on the device only): items of 0.7
+  // of it, but at least 4 tiles of the prefix and 8 own ones (an item costs about two
+  // of either besides), and no more of the prefix than CTAs; each range of a key set
+  // as long as the others. Items are handed out as CTAs ask for them, the prefix's
+  // long ones first. (Dealt out in turn, b64 h32 kv4 d128 behind 16384 keys with own
+  // lengths up to 1024 took 47 us for 41.) A cache far longer than what it holds so
+  // makes few long items: a step of 4096 keys, h32 kv8, takes 13.5 us from a cache of
+  // 4096 rows and 23.4 from one of 131072; of 8 sequences 33 and 42.
   const double share = (1.1 * static_cast<double>(items_p) * kt_p + 0.5 * static_cast<double>(items_o) * kt_o) / 152;
   auto cut = [](int64_t kt, double chunk) -> int64_t {  // the key tiles of an item
     if (kt <= 0) return 1;

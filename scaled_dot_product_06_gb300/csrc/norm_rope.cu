@@ -18,10 +18,11 @@
 // barrier), so the loads in flight hold no registers: with plain loads, four
 // rows a thread ahead of their use, a call at b1 s16384 h32 + 2 x 4, d = 128
 // took 74 us (68% of the copy rate; now 59 us, 85%) and its backward at b4
-// s2048, 3 x 16 heads, 113 us (36%; now 65 us, 62%: its reads are 512-byte
-// pieces, two arrays at once, and a warp waits for three rounds of shuffles a
-// row). Shorter walks than 16 heads lose more to the angles than they gain in
-// grain: 65 us at 8, 72 us at 4, for 60 us of the kernel alone.
+// s2048, 3 x 16 heads, 113 us (36%; now 65 us, 62%: no unit is near its limit,
+// but a warp takes one row at a time, and wait for the copy, the partner's
+// elements, four rounds of two sums' shuffles, the root and the store follow one
+// another, 24 warps an SM). Shorter walks than 16 heads lose more to the angles
+// than they gain in grain: 65 us at 8, 72 us at 4, for 60 us of the kernel alone.
 #include <algorithm>
 
 #include "common.cuh"
