@@ -4,10 +4,12 @@ busy by ordinary products, so that host and device are apart when it matters.
 """
 from __future__ import annotations
 
+from types import SimpleNamespace
+
 import pytest
 import torch
 
-from scaled_dot_product_06_gb300 import (sdpa_bwd, sdpa_bwd_varlen, sdpa_device_error, sdpa_fwd,
+from scaled_dot_product_06_gb300 import (sdpa_bwd, sdpa_bwd_varlen, sdpa_device_error, sdpa_dropout_mask, sdpa_fwd,
                                          sdpa_fwd_prefix, sdpa_fwd_prefix_workspace_size,
                                          sdpa_qk_norm_rope, sdpa_qk_norm_rope_bwd)
 
@@ -172,3 +174,26 @@ def test_captured_on_a_side_stream():
         assert same(got, want)
         del held
     assert sdpa_device_error() == 0
+
+
+def test_keep_bits_on_another_stream(busy):
+    want = sdpa_dropout_mask(2, 4, 96, 128, 0.3, 5, 6)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    kept = busy(s)
+    got = sdpa_dropout_mask(2, 4, 96, 128, 0.3, 5, 6, stream=s)
+    held = overwrite()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    del kept, held
+
+
+def test_foreign_stream_object():
+    """A stream of another library: an object with a handle."""
+    s = torch.cuda.Stream()
+    run = attention_call(20.0)(6)
+    want = [t.clone() for t in run()]
+    torch.cuda.synchronize()
+    got = run(stream=SimpleNamespace(cuda_stream=s.cuda_stream))
+    torch.cuda.synchronize()
+    assert same(got, want)
