@@ -100,11 +100,12 @@ def check_workspace(t: torch.Tensor, device):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _grad(name, t, shape, dtype, device, stream) -> torch.Tensor:
-    """A gradient: the given tensor, checked, or a new one."""
+def _grad(name, t, shape, dtype, device, stream, written=True) -> torch.Tensor:
+    """A gradient: the given tensor, checked where it is written, or a new one."""
     if t is None:
         return new_tensor(shape, dtype, device, stream)
-    _check_io(name, t, shape, dtype, device)
+    if written:
+        _check_io(name, t, shape, dtype, device)
     return t
 
 
@@ -285,9 +286,11 @@ def sdpa_bwd_phases(phases, q, k, v, o, dout, lse, *, scale=None, is_causal=Fals
     if bias is not None:
         _check_io("bias", bias, (1, h, s_q, s_kv), torch.float32, dev)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
-    dq = _grad("dq", dq, q.shape, dt, dev, stream)
-    dk = _grad("dk", dk, k.shape, dt, dev, stream)
-    dv = _grad("dv", dv, v.shape, dt, dev, stream)
+    # (a phase may be given stand-ins for what it does not write)
+    kv = phases & _native.SDPA_BWD_DKDV
+    dq = _grad("dq", dq, q.shape, dt, dev, stream, phases & (_native.SDPA_BWD_DKDV | _native.SDPA_BWD_DQ))
+    dk = _grad("dk", dk, k.shape, dt, dev, stream, kv)
+    dv = _grad("dv", dv, v.shape, dt, dev, stream, kv)
     if bias is not None or dbias is not None:
         dbias = _grad("dbias", dbias, (1, h, s_q, s_kv), torch.float32, dev, stream)
     need = sdpa_bwd_workspace_size(b, h, s_q, s_kv, d_qk, d_v, h_kv, deterministic)
@@ -438,9 +441,11 @@ def sdpa_bwd_phases_varlen(phases, q, k, v, o, dout, lse, seqstart_q, seqstart_k
         _check_io(name, t, shp, dt, dev if t is not q else None)
     _check_io("lse", lse, (h, total_q), torch.float32, dev)
     scale = 1.0 / math.sqrt(d_qk) if scale is None else float(scale)
-    dq = _grad("dq", dq, q.shape, dt, dev, stream)
-    dk = _grad("dk", dk, k.shape, dt, dev, stream)
-    dv = _grad("dv", dv, v.shape, dt, dev, stream)
+    # (a phase may be given stand-ins for what it does not write)
+    kv = phases & _native.SDPA_BWD_DKDV
+    dq = _grad("dq", dq, q.shape, dt, dev, stream, phases & (_native.SDPA_BWD_DKDV | _native.SDPA_BWD_DQ))
+    dk = _grad("dk", dk, k.shape, dt, dev, stream, kv)
+    dv = _grad("dv", dv, v.shape, dt, dev, stream, kv)
     need = sdpa_bwd_varlen_workspace_size(b, h, total_q, d_qk, deterministic)
     if workspace is None:
         workspace = new_tensor(max(need, 1), torch.uint8, dev, stream, scratch=True)

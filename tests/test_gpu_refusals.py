@@ -5,7 +5,8 @@ from __future__ import annotations
 import pytest
 import torch
 
-from scaled_dot_product_06_gb300 import (sdpa_bwd, sdpa_bwd_varlen, sdpa_bwd_workspace_size, sdpa_dropout_mask,
+from scaled_dot_product_06_gb300 import (SDPA_BWD_DKDV, SDPA_BWD_DQ, SDPA_BWD_PREPROCESS, sdpa_bwd, sdpa_bwd_phases,
+                                         sdpa_bwd_varlen, sdpa_bwd_workspace_size, sdpa_dropout_mask,
                                          sdpa_fwd, sdpa_fwd_prefix, sdpa_fwd_prefix_workspace_size, sdpa_fwd_varlen,
                                          sdpa_qk_norm_rope_bwd, sdpa_qk_norm_rope_bwd_workspace_size)
 from scaled_dot_product_06_gb300.inputs import Shape, make_inputs, make_packed_inputs
@@ -98,3 +99,27 @@ def test_around_the_attention():
     for ws in bad_workspaces(need):
         with pytest.raises(ValueError, match="workspace"):
             sdpa_qk_norm_rope_bwd(dy, dy, x, x, None, None, q_weight=w, k_weight=w, workspace=ws)
+
+
+@pytest.mark.parametrize("deterministic", [False, True])
+def test_phases_with_stand_ins(deterministic):
+    """A phase takes stand-ins for the gradients that it does not write."""
+    x = make_inputs(Shape(1, 2, 128, 256, 64, 64), "bf16")
+    q, k, v, do = (x[n].cuda() for n in ("q", "k", "v", "do"))
+    kw = dict(is_causal=True, softcap=20.0, deterministic=deterministic)
+    o, lse = sdpa_fwd(q, k, v, is_causal=True, softcap=20.0)
+    want = sdpa_bwd(q, k, v, o, do, lse, **kw)
+    ws = u8(sdpa_bwd_workspace_size(1, 2, 128, 256, 64, 64, 2, deterministic))
+    one = torch.empty(64, dtype=torch.bfloat16, device="cuda")
+    dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+    call = dict(workspace=ws, **kw)
+    sdpa_bwd_phases(SDPA_BWD_PREPROCESS, q, k, v, o, do, lse, dq=one, dk=one, dv=one, **call)
+    sdpa_bwd_phases(SDPA_BWD_DKDV, q, k, v, o, do, lse, dq=dq, dk=dk, dv=dv, **call)
+    sdpa_bwd_phases(SDPA_BWD_DQ, q, k, v, o, do, lse, dq=dq, dk=dk, dv=dv, **call)
+    torch.cuda.synchronize()
+    assert torch.equal(dk, want[1]) and torch.equal(dv, want[2])
+    if deterministic:
+        assert torch.equal(dq, want[0])
+    for phase, kws in ((SDPA_BWD_DKDV, dict(dq=dq, dk=one, dv=dv)), (SDPA_BWD_DQ, dict(dq=one, dk=dk, dv=dv))):
+        with pytest.raises(ValueError):
+            sdpa_bwd_phases(phase, q, k, v, o, do, lse, **kws, **call)
