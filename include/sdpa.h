@@ -542,6 +542,109 @@ sdpa_status_t sdpa_fwd_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, i
                               size_t workspace_bytes, void* stream);
 
 /*
+ * A key/value cache in pages: a pool of n_pages pages of page_size tokens that
+ * all sequences share. Entry j of a sequence's row of the block table is the
+ * page that holds its tokens j page_size to (j + 1) page_size - 1; a token's
+ * slot is page * page_size + its row of the page.
+ *
+ * sdpa_page_slots gives pages to the new tokens of b requests and builds their
+ * slots, on the device and in one launch:
+ *   seqlens  [b]: tokens of each request in the cache. new_tokens [b]: tokens to
+ *            come, 0 for an idle request, negative for one that has ended.
+ *   block_table  [b, table_width] (table_stride elements between rows), where
+ *            the entries of the new pages are written; no other is. The first
+ *            ceil(seqlens / page_size) of a row are read as its pages.
+ *   free_pages  [n_pages]: a ring of the pages nobody has. Entry i modulo
+ *            n_pages holds one for free_range[0] <= i < free_range[1]; new pages
+ *            are taken from the front, request by request and each in order.
+ *            Pages of ended requests (what their row of the table holds; the row
+ *            itself is left as it is) are written behind the end, and are not
+ *            given out by the same call.
+ *   tokens   either packed (starts not null): `rows` entries, request i's tokens at
+ *            entries starts[i] to starts[i + 1] - 1, starts [b + 1] being an
+ *            output (the sums of new_tokens, held at rows: the offsets that the
+ *            packed calls take), or padded (starts null, rows 0): `width` entries a
+ *            request.
+ *   Outputs  slots: each entry's slot, -1 where it has no token. positions:
+ *            seqlens + the token's number, 0 where there is no token.
+ *            seqlens_out [b]: seqlens + new_tokens, 0 for an ended request.
+ *            free_range_out [2]. seqlens_out may be seqlens and free_range_out
+ *            may be free_range: the call can be captured once and replayed for
+ *            every step. No other two arguments may overlap.
+ *   Refused  a request that needs more pages than are free behind those of the
+ *            requests before it, more than table_width, or more entries than
+ *            there are, gets nothing: its slots are -1 and its seqlens_out is its
+ *            seqlens (requests behind it that need no page are served). A page
+ *            number outside [0, n_pages) gives slots of -1. Negative seqlens
+ *            count as 0.
+ *   Types    int32 device arrays, free_range and free_range_out int64; slots and
+ *            positions 16-byte aligned. n_pages * page_size and table_width *
+ *            page_size below 2^31, b * table_width and b * width at most 2^30.
+ * All outputs are whole numbers and the same in every run.
+ *
+ * sdpa_qk_norm_rope_paged is sdpa_qk_norm_rope with pages as the target: k_pages
+ * and v_pages as sdpa_rows_t {page, row of the page, head}, kv_slots device int32
+ * [b, s], the slot of each token. A token whose slot is outside [0, n_pages *
+ * page_size) is dropped (its query is computed); no other row is touched. Where
+ * two tokens have the same slot, either's row is left. Any page_size.
+ *
+ * sdpa_fwd_paged is the attention of the newest s_q tokens (one in a decoding
+ * step, a few drafted ones) over the pages:
+ *   q, o     [b, h, s_q, d]; lse fp32 [b, h, s_q], as in sdpa_fwd.
+ *   k_pages, v_pages  as sdpa_rows_t {page, row of the page, head}: strides
+ *            positive multiples of 16 bytes, so both [n_pages, h_kv, page_size, d]
+ *            and [n_pages, page_size, h_kv, d] are taken. page_size: a power of
+ *            two, 8 to 2^20. n_pages or table_width 0: there are no keys.
+ *   seqlen_k DEVICE int32 [b]: keys of each sequence, the s_q new tokens' among
+ *            them (appended beforehand); held in [0, table_width * page_size].
+ *            New token t sees the keys p - window_left <= j <= p, p = seqlen_k -
+ *            s_q + t (window_left < 0: from the first). A row that sees no key gets
+ *            O = 0 and LSE = -inf.
+ *   block_table  DEVICE int32 [b, table_width]. Only the entries of pages with a
+ *            key that some new token sees are read. A page number outside [0,
+ *            n_pages) reads as rows of zeros.
+ *            Rows of the pages that no new token sees may hold anything, NaN too.
+ *            Values that only some of the new tokens see must be finite: they
+ *            enter the others' sums with a weight of 0. Keys and queries may be
+ *            NaN: the rows that see one get NaN in O and LSE, no other row does.
+ *   scale    as in sdpa_fwd; softcap 0 (none) or as in the capped calls.
+ *   Heads    h_kv divides h; query head i reads K/V head i / (h / h_kv).
+ *   Workspace  sdpa_fwd_paged_workspace_size(...) bytes, 256-byte aligned, whose
+ *            contents do not matter. Two calls that may run at the same time need
+ *            one each.
+ * The work is cut by the lengths, on the device: neither table_width nor a mix
+ * of lengths costs time. Results are the same bits in every run of the same
+ * call; another batch around a sequence may cut its keys elsewhere and change
+ * the last bit. b, h or s_q of 0: a no-op.
+ */
+sdpa_status_t sdpa_page_slots(int64_t b, int64_t page_size, int64_t table_width,
+                              int64_t table_stride, int64_t n_pages, int64_t rows, int64_t width,
+                              const int32_t* seqlens, const int32_t* new_tokens,
+                              int32_t* block_table, int32_t* free_pages,
+                              const int64_t* free_range, int32_t* slots, int32_t* positions,
+                              int32_t* starts, int32_t* seqlens_out, int64_t* free_range_out,
+                              void* stream);
+sdpa_status_t sdpa_qk_norm_rope_paged(int64_t b, int64_t s, int64_t h, int64_t h_kv, int64_t d,
+                                      int64_t d_v, sdpa_dtype_t dtype, const sdpa_rows_t* q,
+                                      const sdpa_rows_t* k, const sdpa_rows_t* v,
+                                      const sdpa_rows_t* q_out, const sdpa_rows_t* k_pages,
+                                      const sdpa_rows_t* v_pages, int64_t rot, int interleaved,
+                                      const float* cos, const float* sin, int64_t n_pos,
+                                      const int32_t* positions, const void* q_weight,
+                                      const void* k_weight, int weight_fp32, float eps,
+                                      const int32_t* kv_slots, int64_t n_pages, int64_t page_size,
+                                      void* stream);
+size_t sdpa_fwd_paged_workspace_size(int64_t h, int64_t h_kv, int64_t s_q, int64_t d_qk,
+                                     int64_t d_v);
+sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t d_qk,
+                             int64_t d_v, float scale, float softcap, int64_t window_left,
+                             sdpa_dtype_t dtype, const void* q, const sdpa_rows_t* k_pages,
+                             const sdpa_rows_t* v_pages, int64_t n_pages, int64_t page_size,
+                             const int32_t* block_table, int64_t table_width, int64_t table_stride,
+                             const int32_t* seqlen_k, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
  * The backward pass for callers that cannot allocate device memory when they
  * run it (a host framework that owns all GPU memory through its own pool, or
  * a latency-critical loop that cannot afford cudaMalloc's implicit

@@ -9,6 +9,7 @@ from .api import (sdpa_bwd, sdpa_bwd_phases, sdpa_bwd_phases_varlen, sdpa_bwd_va
                   sdpa_bwd_varlen_workspace_size, sdpa_bwd_workspace_size, sdpa_debug_fault,
                   sdpa_device_error, sdpa_dropout_mask, sdpa_fwd, sdpa_fwd_varlen,
                   sdpa_status_string)
+from .paged import sdpa_fwd_paged, sdpa_fwd_paged_workspace_size, sdpa_page_slots
 from .prefix import sdpa_fwd_prefix, sdpa_fwd_prefix_workspace_size
 from .rows import (sdpa_qk_norm_rope, sdpa_qk_norm_rope_bwd, sdpa_qk_norm_rope_bwd_workspace_size)
 
@@ -17,4 +18,5 @@ __all__ = ["sdpa_fwd", "sdpa_bwd", "sdpa_bwd_phases", "SDPA_BWD_PREPROCESS", "SD
            "sdpa_device_error", "sdpa_debug_fault", "sdpa_status_string", "sdpa_fwd_varlen",
            "sdpa_bwd_varlen", "sdpa_bwd_phases_varlen", "sdpa_bwd_varlen_workspace_size",
            "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd", "sdpa_qk_norm_rope_bwd_workspace_size",
-           "sdpa_fwd_prefix", "sdpa_fwd_prefix_workspace_size"]
+           "sdpa_fwd_prefix", "sdpa_fwd_prefix_workspace_size", "sdpa_page_slots", "sdpa_fwd_paged",
+           "sdpa_fwd_paged_workspace_size"]

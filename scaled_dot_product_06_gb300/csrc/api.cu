@@ -17,6 +17,7 @@
 
 #include "../../include/sdpa.h"
 #include "common.cuh"
+#include "host.cuh"
 #include "prefix.cuh"
 
 namespace {
@@ -217,6 +218,9 @@ uint32_t drop_threshold(float p) {
 }  // namespace
 
 namespace sdpa {
+sdpa_status_t tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) { return encoder(out); }
+sdpa_status_t device_error_word(uint32_t** out) { return error_word_ptr(out); }
+
 void set_last_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
 
 cudaError_t prepare_kernel(const void* kern, int smem, int regs) {
@@ -297,7 +301,7 @@ sdpa_status_t check_alibi(const Mask& mk, int64_t b, int64_t h) {
 // softcap - 2 softcap r with r in (0, 1) off by 2^-21 relative, so above 4096
 // the score would be off by more than 2^-8, which is a bf16 rounding of P (of
 // fp16's, 2^-11, it is more above 512).
-constexpr float kMaxSoftcap = 4096.f;
+constexpr float kMaxSoftcap = kSoftcapMost;
 sdpa_status_t check_softcap(const Mask& mk, float scale) {
   if (!mk.capped) return SDPA_OK;
   if (!(mk.softcap > 0.f && mk.softcap <= kMaxSoftcap))

@@ -205,13 +205,20 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_fwd_kernel(const __grid
     if (i < un.n) copy16(&ring[i][threadIdx.x], src + i * k.token.sh, un.live);
     copy_commit();
   }
-  int64_t row = un.t;
+  int64_t row = un.t, outer = un.b;
   bool store = un.live;
   if (k.cached) {
-    row += un.live ? __ldg(p.kv_rows + un.b) : 0;
-    store = un.live && row >= 0 && row < p.cache_rows;
+    if (p.kv_slots != nullptr) {
+      const uint32_t slot = un.live ? static_cast<uint32_t>(__ldg(p.kv_slots + un.token)) : 0u;
+      outer = slot / p.page_size;
+      row = slot % p.page_size;
+      store = un.live && slot < p.n_slots;  // (negative slots are large ones here)
+    } else {
+      row += un.live ? __ldg(p.kv_rows + un.b) : 0;
+      store = un.live && row >= 0 && row < p.cache_rows;
+    }
   }
-  uint16_t* dst = static_cast<uint16_t*>(k.head.ptr) + un.b * k.head.sb + row * k.head.st + un.h0 * k.head.sh + 8 * l;
+  uint16_t* dst = static_cast<uint16_t*>(k.head.ptr) + outer * k.head.sb + row * k.head.st + un.h0 * k.head.sh + 8 * l;
   const bool normed = k.weight != nullptr, rotate = k.rotate != 0;
   const int64_t pos = (rotate && p.positions != nullptr && un.live) ? __ldg(p.positions + un.token) : un.t;
   float cw[8], sw[8];  // the angles times the weights of the element and of its partner

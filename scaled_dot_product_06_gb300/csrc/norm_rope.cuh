@@ -21,7 +21,7 @@ struct RowKind {
   const void* weight;  // [d] norm weight or null: no norm
   int heads, width;    // heads; elements a row (the values' may be fewer than d)
   int rotate;          // whether the rows are rotated
-  int cached;          // head-side row = kv_rows[batch] + token instead of token
+  int cached;          // head-side row = kv_rows[batch] + token, or from kv_slots, instead of token
   int block0;          // first block of this kind
   uint32_t units;      // its work units, one a warp at a time
 };
@@ -41,6 +41,11 @@ struct NormRopeParams {
   const int* positions;  // [tokens] or null: the token's number in its sequence
   const int* kv_rows;    // [b] or null
   int64_t cache_rows;    // rows of the caches
+  // pages instead of caches: token t's row is row slot % page_size of page
+  // slot / page_size (head.sb is then the stride of the pages)
+  const int* kv_slots;   // [tokens] or null
+  uint32_t page_size;
+  uint32_t n_slots;      // rows of all pages
   // backward: head = dy, token = dx, x = the forward's input; fp32 partial weight
   // gradients, one row of d per block of kinds 0 and 1
   RowSet x[3];

@@ -39,6 +39,7 @@ RowSet row_set(const sdpa_rows_t* r, int64_t n_batch, int64_t n_row, int64_t n_h
 }
 
 constexpr int64_t kMaxTokens = (int64_t{1} << 30);
+constexpr int64_t kMaxSlots = (int64_t{1} << 31) - 1;  // slots are int32
 
 // Checks shared by both directions that need no row pointer; *empty: no tokens.
 sdpa_status_t check_common(int64_t b, int64_t s, int64_t h, int64_t h_kv, int64_t d, int64_t d_v, int dtype,
@@ -84,6 +85,63 @@ void fill_common(NormRopeParams* p, int64_t b, int64_t s, int64_t d, int64_t rot
   p->positions = positions;
 }
 
+// Where the keys and values go: new tensors, caches (rows) or pages (slots).
+struct Target {
+  const int32_t* kv_rows = nullptr;
+  int64_t cache_rows = 0;
+  const int32_t* kv_slots = nullptr;
+  int64_t n_pages = 0, page_size = 0;
+};
+
+sdpa_status_t forward(int64_t b, int64_t s, int64_t h, int64_t h_kv, int64_t d, int64_t d_v, sdpa_dtype_t dtype,
+                      const sdpa_rows_t* q, const sdpa_rows_t* k, const sdpa_rows_t* v, const sdpa_rows_t* q_out,
+                      const sdpa_rows_t* k_out, const sdpa_rows_t* v_out, int64_t rot, int interleaved,
+                      const float* cos, const float* sin, int64_t n_pos, const int32_t* positions,
+                      const void* q_weight, const void* k_weight, int weight_fp32, float eps, const Target& to,
+                      void* stream) {
+  bool empty = false;
+  if (sdpa_status_t st = check_common(b, s, h, h_kv, d, d_v, dtype, rot, cos, sin, n_pos, positions, q_weight,
+                                      k_weight, eps, &empty))
+    return st;
+  if ((v == nullptr) != (v_out == nullptr)) return fail(SDPA_ERR_INVALID_ARG, "v and v_out go together");
+  if (to.cache_rows < 0 || to.cache_rows > kMaxTokens) return fail(SDPA_ERR_INVALID_ARG, "cache_rows");
+  if (empty) return SDPA_OK;
+  if (((reinterpret_cast<uintptr_t>(to.kv_rows) | reinterpret_cast<uintptr_t>(to.kv_slots)) & 3u) != 0)
+    return fail(SDPA_ERR_MISALIGNED, to.kv_slots != nullptr ? "kv_slots" : "kv_rows");
+  // extents of the outer and row dimensions that k_out and v_out have
+  const bool paged = to.kv_slots != nullptr, cached = paged || to.kv_rows != nullptr;
+  const int64_t kv_outer = paged ? to.n_pages : b;
+  const int64_t kv_out_rows = paged ? to.page_size : to.kv_rows != nullptr ? to.cache_rows : s;
+  const bool to_kv = !paged || to.n_pages > 0;  // (no page: no row of theirs is touched)
+  sdpa_status_t st = check_rows(q, b, s, h, "q");
+  if (!st) st = check_rows(k, b, s, h_kv, "k");
+  if (!st && v != nullptr) st = check_rows(v, b, s, h_kv, "v");
+  if (!st) st = check_rows(q_out, b, s, h, "q_out");
+  if (!st && to_kv) st = check_rows(k_out, kv_outer, kv_out_rows, h_kv, "k_out");
+  if (!st && to_kv && v != nullptr) st = check_rows(v_out, kv_outer, kv_out_rows, h_kv, "v_out");
+  if (st) return st;
+
+  NormRopeParams p{};
+  fill_common(&p, b, s, d, rot, interleaved, cos, sin, n_pos, positions, weight_fp32, eps);
+  p.kv_rows = to.kv_rows;
+  p.cache_rows = to.cache_rows;
+  p.kv_slots = to.kv_slots;
+  p.page_size = static_cast<uint32_t>(to.page_size);
+  p.n_slots = static_cast<uint32_t>(to.n_pages * to.page_size);
+  const int hi = static_cast<int>(h), hk = static_cast<int>(h_kv), di = static_cast<int>(d);
+  auto kv_to = [&](const sdpa_rows_t* r) { return to_kv ? row_set(r, kv_outer, kv_out_rows, h_kv) : RowSet{}; };
+  p.n_kinds = v != nullptr ? 3 : 2;
+  p.kind[0] = RowKind{row_set(q, b, s, h), row_set(q_out, b, s, h), q_weight, hi, di, rot > 0, 0, 0, 0};
+  p.kind[1] = RowKind{row_set(k, b, s, h_kv), kv_to(k_out), k_weight, hk, di, rot > 0, cached, 0, 0};
+  if (v != nullptr)
+    p.kind[2] = RowKind{row_set(v, b, s, h_kv), kv_to(v_out), nullptr, hk, static_cast<int>(d_v), 0, cached, 0, 0};
+  const int blocks = norm_rope_plan(&p, false);
+  if (blocks < 0) return fail(SDPA_ERR_UNSUPPORTED, "too many rows");
+  const cudaError_t e = launch_norm_rope_fwd(dtype == SDPA_BF16, p, blocks, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, cudaGetErrorString(e));
+  return SDPA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -95,41 +153,30 @@ sdpa_status_t sdpa_qk_norm_rope(int64_t b, int64_t s, int64_t h, int64_t h_kv, i
                                 const float* sin, int64_t n_pos, const int32_t* positions, const void* q_weight,
                                 const void* k_weight, int weight_fp32, float eps, const int32_t* kv_rows,
                                 int64_t cache_rows, void* stream) {
-  bool empty = false;
-  if (sdpa_status_t st = check_common(b, s, h, h_kv, d, d_v, dtype, rot, cos, sin, n_pos, positions, q_weight,
-                                      k_weight, eps, &empty))
-    return st;
-  if ((v == nullptr) != (v_out == nullptr)) return fail(SDPA_ERR_INVALID_ARG, "v and v_out go together");
-  if (cache_rows < 0 || cache_rows > kMaxTokens) return fail(SDPA_ERR_INVALID_ARG, "cache_rows");
-  if (empty) return SDPA_OK;
-  if ((reinterpret_cast<uintptr_t>(kv_rows) & 3u) != 0) return fail(SDPA_ERR_MISALIGNED, "kv_rows");
-  const int64_t kv_out_rows = kv_rows != nullptr ? cache_rows : s;
-  sdpa_status_t st = check_rows(q, b, s, h, "q");
-  if (!st) st = check_rows(k, b, s, h_kv, "k");
-  if (!st && v != nullptr) st = check_rows(v, b, s, h_kv, "v");
-  if (!st) st = check_rows(q_out, b, s, h, "q_out");
-  if (!st) st = check_rows(k_out, b, kv_out_rows, h_kv, "k_out");
-  if (!st && v != nullptr) st = check_rows(v_out, b, kv_out_rows, h_kv, "v_out");
-  if (st) return st;
+  Target to;
+  to.kv_rows = kv_rows;
+  to.cache_rows = cache_rows;
+  return forward(b, s, h, h_kv, d, d_v, dtype, q, k, v, q_out, k_out, v_out, rot, interleaved, cos, sin, n_pos,
+                 positions, q_weight, k_weight, weight_fp32, eps, to, stream);
+}
 
-  NormRopeParams p{};
-  fill_common(&p, b, s, d, rot, interleaved, cos, sin, n_pos, positions, weight_fp32, eps);
-  p.kv_rows = kv_rows;
-  p.cache_rows = cache_rows;
-  const int hi = static_cast<int>(h), hk = static_cast<int>(h_kv), di = static_cast<int>(d);
-  const int cached = kv_rows != nullptr ? 1 : 0;
-  p.n_kinds = v != nullptr ? 3 : 2;
-  p.kind[0] = RowKind{row_set(q, b, s, h), row_set(q_out, b, s, h), q_weight, hi, di, rot > 0, 0, 0, 0};
-  p.kind[1] = RowKind{row_set(k, b, s, h_kv), row_set(k_out, b, kv_out_rows, h_kv), k_weight, hk, di, rot > 0,
-                      cached, 0, 0};
-  if (v != nullptr)
-    p.kind[2] = RowKind{row_set(v, b, s, h_kv), row_set(v_out, b, kv_out_rows, h_kv), nullptr, hk,
-                        static_cast<int>(d_v), 0, cached, 0, 0};
-  const int blocks = norm_rope_plan(&p, false);
-  if (blocks < 0) return fail(SDPA_ERR_UNSUPPORTED, "too many rows");
-  const cudaError_t e = launch_norm_rope_fwd(dtype == SDPA_BF16, p, blocks, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, cudaGetErrorString(e));
-  return SDPA_OK;
+sdpa_status_t sdpa_qk_norm_rope_paged(int64_t b, int64_t s, int64_t h, int64_t h_kv, int64_t d, int64_t d_v,
+                                      sdpa_dtype_t dtype, const sdpa_rows_t* q, const sdpa_rows_t* k,
+                                      const sdpa_rows_t* v, const sdpa_rows_t* q_out, const sdpa_rows_t* k_pages,
+                                      const sdpa_rows_t* v_pages, int64_t rot, int interleaved, const float* cos,
+                                      const float* sin, int64_t n_pos, const int32_t* positions,
+                                      const void* q_weight, const void* k_weight, int weight_fp32, float eps,
+                                      const int32_t* kv_slots, int64_t n_pages, int64_t page_size, void* stream) {
+  if (n_pages < 0 || page_size < 1) return fail(SDPA_ERR_INVALID_ARG, "n_pages, page_size");
+  if (n_pages > kMaxSlots || page_size > kMaxSlots || n_pages * page_size > kMaxSlots)
+    return fail(SDPA_ERR_UNSUPPORTED, "too many rows of pages");
+  if (kv_slots == nullptr && b > 0 && s > 0) return fail(SDPA_ERR_INVALID_ARG, "kv_slots");
+  Target to;
+  to.kv_slots = kv_slots;
+  to.n_pages = n_pages;
+  to.page_size = page_size;
+  return forward(b, s, h, h_kv, d, d_v, dtype, q, k, v, q_out, k_pages, v_pages, rot, interleaved, cos, sin,
+                 n_pos, positions, q_weight, k_weight, weight_fp32, eps, to, stream);
 }
 
 size_t sdpa_qk_norm_rope_bwd_workspace_size(int64_t b, int64_t s, int64_t h, int64_t h_kv, int64_t d, int64_t d_v) {

@@ -1,0 +1,278 @@
+// Block tables and slot maps of a paged cache, built from request lengths.
+//
+// Request i has n tokens cached and x new ones; with pages of P tokens
+//   have = ceil(n / P),  need = ceil((n + x) / P),  k = need - have
+// pages are asked for, and page have + j of the request is entry
+//   head + sum_{i' < i} k_i' + j   (modulo the pool)
+// of the ring of free pages. New token t lies at
+//   slot = table[i][(n + t) / P] P + (n + t) mod P.
+// Ended requests' pages go behind the ring's tail in the same way. So three
+// sums over the requests (tokens, pages asked for, pages given back) are all
+// that one entry needs of the others.
+//
+// Nothing here is worth more than a launch and three trips to memory (lengths,
+// then pages, then the stores): one cluster of CTAs, each of which scans all
+// requests, 1024 at a time, and then takes its share of the tokens and table
+// entries, found by bisection of the sums in shared memory. A cluster, since
+// the lengths and the ring's counters may be advanced in place: they are
+// written after a barrier of all that read them.
+#include "common.cuh"
+#include "page_slots.cuh"
+
+namespace sdpa {
+
+namespace {
+
+constexpr int kReq = 1024;  // threads, and requests scanned at a time
+constexpr int kWarps = kReq / 32;
+// Calls of more entries are shared by a cluster: a CTA takes 4096 in one go, and
+// the cluster's barrier costs about as much as another.
+constexpr int kCluster = 8;
+constexpr int64_t kAlone = 8192;
+
+__device__ __forceinline__ uint32_t ceil_div(uint32_t a, uint32_t b) { return a / b + (a % b != 0 ? 1u : 0u); }
+
+// Sums of tokens (held at `cap`, so that they stay in 32 bits; they matter only up
+// to the rows there are), pages asked for, pages given back.
+struct Sums {
+  uint32_t tok, take, back;
+};
+__device__ __forceinline__ Sums add(const Sums& a, const Sums& b, uint32_t cap) {
+  return Sums{min(a.tok + b.tok, cap), a.take + b.take, a.back + b.back};
+}
+__device__ __forceinline__ Sums up(const Sums& s, int o) {
+  return Sums{__shfl_up_sync(0xffffffffu, s.tok, o), __shfl_up_sync(0xffffffffu, s.take, o),
+              __shfl_up_sync(0xffffffffu, s.back, o)};
+}
+
+struct Shared {
+  uint32_t tok_end[kReq], take_end[kReq], back_end[kReq];  // inclusive sums
+  uint32_t len[kReq], add[kReq], take[kReq];               // cached tokens, new ones, pages asked for
+  uint8_t served[kReq];
+  Sums warp[kWarps];
+  Sums carry;
+};
+
+// The first of n entries above x (n: none).
+__device__ __forceinline__ int above(const uint32_t* ends, int n, uint32_t x) {
+  int lo = 0;
+  for (int step = kReq / 2; step > 0; step >>= 1)
+    if (lo + step <= n && ends[lo + step - 1] <= x) lo += step;
+  return lo < n && ends[lo] <= x ? lo + 1 : lo;
+}
+
+__global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_constant__ PageSlotsParams p) {
+  __shared__ Shared s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ctas = gridDim.x, first = blockIdx.x * kReq + tid, step = ctas * kReq;
+  const uint32_t page = static_cast<uint32_t>(p.page);
+  const bool packed = p.packed != 0;
+  const uint32_t rows = static_cast<uint32_t>(p.rows), cap = packed ? rows + 1u : 0u;
+  const int64_t head = p.range[0], tail = p.range[1];
+  // (any contents of the counters stay inside the ring)
+  const uint32_t avail =
+      tail <= head ? 0u : static_cast<uint32_t>(min(static_cast<uint64_t>(tail) - static_cast<uint64_t>(head),
+                                                    static_cast<uint64_t>(p.pool)));
+  const uint32_t head0 = p.pool > 0 ? static_cast<uint32_t>(static_cast<uint64_t>(head) % p.pool) : 0u;
+  const uint32_t tail0 = p.pool > 0 ? static_cast<uint32_t>(static_cast<uint64_t>(tail) % p.pool) : 0u;
+  auto ring_at = [&](uint32_t from, uint32_t i) {  // i < pool
+    const uint32_t at = from + i;
+    return at >= p.pool ? at - p.pool : at;
+  };
+
+  Sums before{0u, 0u, 0u};  // of the requests before this chunk
+  uint32_t taken = 0;       // pages taken by served requests
+  int len_out = 0;
+  // Scans requests r0 .. r0 + kReq - 1 into s; returns this thread's new length.
+  auto scan = [&](int r0) -> int {
+    const int r = r0 + tid;
+    const bool live = r < p.b;
+    const int n_in = live ? p.seqlens[r] : 0, x = live ? p.new_tokens[r] : 0;
+    const uint32_t n = static_cast<uint32_t>(max(n_in, 0)), more = static_cast<uint32_t>(max(x, 0));
+    const uint32_t have = ceil_div(n, page), need = ceil_div(n + more, page);
+    const uint32_t wide = static_cast<uint32_t>(p.width);
+    const bool room = live && x >= 0 && need <= wide;
+    // (a padded request asks for pages when its tokens have entries; a packed one's
+    // place is known after the sum, and where there is no room for it none of those
+    // behind it has any, so that what it asks for changes nothing)
+    const bool padded_fits = packed || more <= static_cast<uint32_t>(p.per);
+    Sums mine{packed ? min(more, cap) : 0u, room && padded_fits ? need - have : 0u,
+              live && x < 0 ? min(have, wide) : 0u};
+    const uint32_t asked = mine.take;
+    Sums sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sums u = up(sum, o);
+      if (lane >= o) sum = add(sum, u, cap);
+    }
+    if (lane == 31) s.warp[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      Sums w = s.warp[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const Sums u = up(w, o);
+        if (lane >= o) w = add(w, u, cap);
+      }
+      s.warp[lane] = w;
+    }
+    __syncthreads();
+    if (warp > 0) sum = add(sum, s.warp[warp - 1], cap);
+    sum = add(sum, before, cap);
+    const bool fits = room && (packed ? sum.tok <= rows : padded_fits);
+    const bool served = fits && (asked == 0 || sum.take <= avail);
+    s.tok_end[tid] = sum.tok;
+    s.take_end[tid] = sum.take;
+    s.back_end[tid] = sum.back;
+    s.len[tid] = n;
+    s.add[tid] = more;
+    s.take[tid] = asked;
+    s.served[tid] = served ? 1 : 0;
+    // served requests are the first ones in the order of their pages: the most taken is
+    // the last one's sum
+    const uint32_t upto = __reduce_max_sync(0xffffffffu, served && asked > 0 ? sum.take : 0u);
+    if (tid == kReq - 1) s.carry = sum;
+    __syncthreads();
+    if (lane == 0) s.warp[warp].tok = upto;
+    __syncthreads();
+    taken = max(taken, __reduce_max_sync(0xffffffffu, s.warp[lane].tok));
+    return x < 0 ? 0 : static_cast<int>(served ? n + more : n);
+  };
+
+  for (int r0 = 0; r0 < p.b; r0 += kReq) {
+    len_out = scan(r0);
+    const int n_req = min(kReq, p.b - r0);
+    const Sums after = s.carry;
+    // the page ids of new pages, from the ring
+    auto fresh = [&](uint32_t i) { return p.ring[ring_at(head0, i)]; };
+    // ---- tokens, four at a time
+    const uint32_t lo = packed ? min(before.tok, rows)
+                                   : static_cast<uint32_t>(r0) * static_cast<uint32_t>(p.per);
+    const uint32_t hi = packed ? min(after.tok, rows)
+                                   : static_cast<uint32_t>(r0 + n_req) * static_cast<uint32_t>(p.per);
+    for (uint32_t g = lo / 4 + first; g < ceil_div(hi, 4); g += step) {
+      int slot[4], pos[4];
+      int i = 0;           // request of the chunk
+      uint32_t end = 0;    // its last entry + 1 (0: none yet)
+      uint32_t at = 0;     // page of the token before
+      int id = -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t r = 4 * g + e;
+        slot[e] = -1;
+        pos[e] = 0;
+        if (r < lo || r >= hi) continue;
+        bool turn = false;  // another request's first token here
+        if (r >= end) {
+          if (packed) {
+            i = above(s.tok_end, n_req, r);
+            end = s.tok_end[i];
+          } else {
+            i = static_cast<int>(r / static_cast<uint32_t>(p.per)) - r0;
+            end = static_cast<uint32_t>(r0 + i + 1) * static_cast<uint32_t>(p.per);
+          }
+          turn = true;
+        }
+        // (packed: entries of a request are as many as its tokens; the one cut off by
+        // the last row has its sum held there, and its place from its first entry)
+        const uint32_t start = packed ? (i > 0 ? s.tok_end[i - 1] : before.tok)
+                                          : end - static_cast<uint32_t>(p.per);
+        const uint32_t t = r - start;
+        if (t >= s.add[i]) continue;
+        const uint32_t place = s.len[i] + t, pg = place / page, off = place - pg * page;
+        pos[e] = static_cast<int>(place);
+        if (!s.served[i]) continue;
+        if (turn || id < 0 || pg != at) {
+          at = pg;
+          const uint32_t have = ceil_div(s.len[i], page);
+          id = pg < have ? p.table[(r0 + i) * p.table_stride + pg]
+                         : fresh(s.take_end[i] - s.take[i] + pg - have);
+        }
+        if (id >= 0 && static_cast<uint32_t>(id) < p.pool) slot[e] = static_cast<int>(id * page + off);
+      }
+      if (4 * g >= lo && 4 * g + 4 <= hi) {
+        reinterpret_cast<int4*>(p.slots)[g] = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        reinterpret_cast<int4*>(p.positions)[g] = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t r = 4 * g + e;
+          if (r >= lo && r < hi) {
+            p.slots[r] = slot[e];
+            p.positions[r] = pos[e];
+          }
+        }
+      }
+    }
+    // ---- new entries of the table
+    for (uint32_t e = before.take + first; e < min(after.take, avail); e += step) {
+      const int i = above(s.take_end, n_req, e);
+      if (!s.served[i]) continue;
+      const uint32_t j = e - (s.take_end[i] - s.take[i]);
+      p.table[(r0 + i) * p.table_stride + ceil_div(s.len[i], page) + j] = fresh(e);
+    }
+    // ---- pages given back
+    for (uint32_t e = before.back + first; e < after.back; e += step) {
+      const int i = above(s.back_end, n_req, e);
+      const uint32_t j = e - (i > 0 ? s.back_end[i - 1] : before.back);
+      if (p.pool > 0) p.ring[ring_at(tail0, e % p.pool)] = p.table[(r0 + i) * p.table_stride + j];
+    }
+    if (packed && blockIdx.x == 0) {
+      if (r0 == 0 && tid == 0) p.starts[0] = 0;
+      if (tid < n_req) p.starts[r0 + tid + 1] = static_cast<int>(min(s.tok_end[tid], rows));
+    }
+    before = after;
+    __syncthreads();  // s is free again
+  }
+  if (packed) {  // behind the last token
+    if (p.b == 0 && first == 0) p.starts[0] = 0;
+    for (uint32_t r = before.tok + first; r < rows; r += step) {
+      p.slots[r] = -1;
+      p.positions[r] = 0;
+    }
+  }
+  // ---- what may be advanced in place, after all have read it
+  if (ctas > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+  if (blockIdx.x != 0) return;
+  if (p.b <= kReq) {
+    if (tid < p.b) p.seqlens_out[tid] = len_out;
+  } else {
+    const Sums all = before;
+    before = Sums{0u, 0u, 0u};
+    for (int r0 = 0; r0 < p.b; r0 += kReq) {
+      const int n = scan(r0);
+      if (r0 + tid < p.b) p.seqlens_out[r0 + tid] = n;
+      before = s.carry;
+      __syncthreads();
+    }
+    before = all;
+  }
+  if (tid == 0) {
+    p.range_out[0] = head + taken;
+    p.range_out[1] = tail + before.back;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_page_slots(const PageSlotsParams& p, cudaStream_t st) {
+  const int64_t entries = p.packed ? p.rows : static_cast<int64_t>(p.b) * p.per;
+  const unsigned ctas = entries > kAlone ? kCluster : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kReq);
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ctas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, page_slots_kernel, p);
+}
+
+}  // namespace sdpa

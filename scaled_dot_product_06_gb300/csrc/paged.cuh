@@ -1,0 +1,53 @@
+// Parameters and launchers of the attention over a paged cache (paged_kernel.cuh,
+// paged_join.cu).
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace sdpa {
+
+constexpr int kPagedTile = 128;   // keys a tile
+constexpr int kPagedBox = 64;     // most keys of one copy
+constexpr int kPagedCost = 1;     // what a unit costs besides its key tiles, in tiles
+constexpr int kPagedGrid = 152;   // CTAs at most: one an SM
+
+// A unit of work is a sequence, a K/V head and a block of its query rows. The
+// units of all sequences, each as long as its key tiles and kPagedCost, are one
+// line that is cut into as many equal runs as there are CTAs.
+struct PagedParams {
+  int B, H_kv;
+  int R, s_q;              // query rows of a K/V head: (h / h_kv) * s_q, row x of token x % s_q
+  int row_blocks;          // blocks of the rows
+  int page_shift;          // log2 of the tokens a page
+  int box, box_shift;      // keys a copy: the page's, at most kPagedBox
+  int n_pages;             // pages of the pool
+  int64_t table_stride;
+  int capacity;            // tokens a row of the table can hold
+  int left;                // keys before a token that it sees, < 0: all
+  const int* table;
+  const int* seqlen;
+  float scale_log2;        // factor of the raw score in the exponent
+  float cap_in, lse_shift; // capped scores: see cap_r8; lse_shift = softcap log2(e)
+  int capped;
+  uint32_t q_box;          // bytes of a 64-column box of Q
+  int grid;
+  // Partial rows of units cut by a run's end: run c leaves slot 2 c for the
+  // unit it begins within and slot 2 c + 1 for the one it ends within.
+  float* part;             // [2 grid][rows a block][d_v]
+  float* part_lse;         // [2 grid][rows a block], base 2
+  // {unit + 1 of slot 2 c or 0, 1 if the unit ends there, unit + 1 of slot 2 c + 1 or 0, 0}
+  int4* runs;              // [grid]
+  void* o;
+  float* lse;
+  uint32_t* err;
+};
+
+// Rows a block: the columns of the score tiles, a multiple of 16.
+__host__ __device__ constexpr int paged_rows(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+
+cudaError_t launch_paged_bf16(int d_qk, int d_v, const CUtensorMap (&m)[3], const PagedParams& p, cudaStream_t st);
+cudaError_t launch_paged_fp16(int d_qk, int d_v, const CUtensorMap (&m)[3], const PagedParams& p, cudaStream_t st);
+cudaError_t launch_paged_join(bool bf16, int d_v, const PagedParams& p, cudaStream_t st);
+
+}  // namespace sdpa

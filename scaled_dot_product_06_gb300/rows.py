@@ -95,8 +95,8 @@ def _check_qkv(q, k, v):
 
 
 def sdpa_qk_norm_rope(q, k, cos, sin, *, v=None, positions=None, q_weight=None, k_weight=None,
-                      eps=1e-6, interleaved=False, kv_rows=None, q_out=None, k_out=None, v_out=None,
-                      stream=None):
+                      eps=1e-6, interleaved=False, kv_rows=None, kv_slots=None, q_out=None, k_out=None,
+                      v_out=None, stream=None):
     """Root-mean-square norm of each query and key head, and its rotation by
     position, from the projection's layout to the attention's in one pass.
 
@@ -110,7 +110,11 @@ def sdpa_qk_norm_rope(q, k, cos, sin, *, v=None, positions=None, q_weight=None, 
     (both fp32 or both of q's dtype) scale the normalised heads; None leaves
     that side unnormalised. kv_rows (int32 [b]) makes k_out and v_out caches
     [b, h_kv, rows, d] that get token t of sequence i in row kv_rows[i] + t
-    (tokens outside the cache are dropped, no other row is touched)."""
+    (tokens outside the cache are dropped, no other row is touched).
+    kv_slots (int32 [b, s]) makes them the pages [n_pages, h_kv, page_size, d] of
+    a paged cache instead: each token goes to row slot % page_size of page
+    slot // page_size, or nowhere where the slot is outside the pages (see
+    sdpa_page_slots)."""
     _check_qkv(q, k, v)
     b, s, h, d = q.shape
     h_kv, dt, dev = k.shape[2], q.dtype, q.device
@@ -122,14 +126,23 @@ def sdpa_qk_norm_rope(q, k, cos, sin, *, v=None, positions=None, q_weight=None, 
         raise ValueError("v_out without v")
     rot, cos_p, sin_p, n_pos, pos_p = _table(dev, cos, sin, positions, b, s)
     qw_p, kw_p, fp32 = _weights(dt, dev, q_weight, k_weight, d)
-    cache, rows_p = s, None
-    if kv_rows is not None:
+    outer, cache, rows_p = b, s, None
+    if kv_slots is not None:
+        if kv_rows is not None:
+            raise ValueError("either kv_rows or kv_slots")
+        rows_p = check_flat("kv_slots", kv_slots, (b, s), torch.int32, dev)
+        if k_out is None or (v is not None and v_out is None):
+            raise ValueError("kv_slots needs the pages as k_out (and v_out)")
+        if k_out.dim() != 4:
+            raise ValueError("k_out must have 4 dimensions")
+        outer, _, cache, _ = k_out.shape
+    elif kv_rows is not None:
         rows_p = check_flat("kv_rows", kv_rows, (b,), torch.int32, dev)
         if k_out is None or (v is not None and v_out is None):
             raise ValueError("kv_rows needs the caches as k_out (and v_out)")
         cache = k_out.shape[2] if k_out.dim() == 4 else -1
     # outputs: new ones are contiguous
-    row, kv_shape = d, (b, h_kv, cache, d)
+    row, kv_shape = d, (outer, h_kv, cache, d)
     if q_out is None:
         q_out = new_tensor((b, h, s, d), dt, dev, stream)
         q_to = _pack_rows(q_out.data_ptr(), h * s * row, row, s * row)
@@ -148,7 +161,12 @@ def sdpa_qk_norm_rope(q, k, cos, sin, *, v=None, positions=None, q_weight=None, 
             v_out = new_tensor((b, h_kv, s, d_v), dt, dev, stream)
         else:
             _check_output("v_out", v_out)
-        v_to = _head_rows("v_out", v_out, (b, h_kv, cache, d_v), dt, dev)
+        v_to = _head_rows("v_out", v_out, (outer, h_kv, cache, d_v), dt, dev)
+    if kv_slots is not None:
+        _run(q, "sdpa_qk_norm_rope_paged", b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], q_in, k_in, v_in, q_to, k_to,
+             v_to, rot, int(bool(interleaved)), cos_p, sin_p, n_pos, pos_p, qw_p, kw_p, fp32, eps, rows_p, outer,
+             cache, _stream_ptr(stream, q))
+        return q_out, k_out, v_out
     _run(q, "sdpa_qk_norm_rope", b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], q_in, k_in, v_in, q_to, k_to, v_to,
          rot, int(bool(interleaved)), cos_p, sin_p, n_pos, pos_p, qw_p, kw_p, fp32, eps, rows_p, cache,
          _stream_ptr(stream, q))
