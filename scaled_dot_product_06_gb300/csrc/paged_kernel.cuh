@@ -24,12 +24,23 @@
 // at most two slots a CTA, joined by a second kernel (paged_join.cu); the others
 // are written as they are.
 //
-// One persistent CTA an SM. Roles: a warpgroup of softmax threads (two at N = 64,
-// 32 rows each), a producer warp (walks the run, tells the others its units through a
-// ring, copies pages by TMA, its lanes one box of a page each), an MMA issuer.
+// One persistent CTA an SM. Roles: two warpgroups of softmax threads (at N = 16 they
+// take the key tiles in turns, each with a maximum, sum and O of its own, joined at
+// the unit's end by the one that had the last tile, while the other goes on; at 32
+// and 64 each has half of the rows), two producer warps, which both walk the run and
+// copy pages by TMA, one the keys, the other the values (a copy of a small page
+// takes its warp longer to issue than memory to deliver), and two MMA issuers, one for
+// S^T, up to two tiles ahead, one for O^T: the products are so small that a tile's
+// instructions and waits, not the tensor cores, bound an issuer (1900 cycles a tile
+// of d = 64 for one warp with both). The keys' producer also copies the queries and
+// tells the others the units through a ring.
 // Rows of a tile that no query sees (behind the last key, before the window,
-// in pages that are not read) may hold anything: their scores are masked, and
-// their values are zeroed in shared memory, since P's zeros would not cancel them.
+// in pages that are not read) may hold anything. Their scores are masked; their
+// values, which P's zeros would not cancel, are left out of the product 16 keys at
+// a time, and zeroed in shared memory within such a step, by the MMA issuer, which
+// waits for the values anyway. (Zeroed by the softmax threads, which then had to wait
+// for them too, 256 sequences of up to 777 keys took 209 us for 16 heads of their
+// own, where whole tiles of as many bytes took 131.)
 #pragma once
 #include "common.cuh"
 #include "paged.cuh"
@@ -39,17 +50,18 @@ namespace sdpa {
 template <int DQK, int DV, int N>
 struct PagedCfg {
   static constexpr int BN = kPagedTile;
-  static constexpr int GROUPS = N == 64 ? 2 : 1;       // softmax warpgroups
-  static constexpr int NC = N / GROUPS;                // rows a thread
-  static constexpr int SOFT = 128 * GROUPS;            // softmax threads
-  static constexpr int THREADS = SOFT + 64;
+  static constexpr bool TURNS = N == 16;               // the warpgroups take tiles in turns, else half of the rows each
+  static constexpr int NC = TURNS ? N : N / 2;         // rows a thread
+  static constexpr int SOFT = 256;                     // softmax threads
+  static constexpr int THREADS = SOFT + 128;
   static constexpr int K_BYTES = BN * DQK * 2;
   static constexpr int V_BYTES = BN * DV * 2;
   static constexpr int Q_BYTES = N * DQK * 2;
   static constexpr int P_PITCH = N * 2;                // bytes a key of P^T: the swizzle's width
   static constexpr int P_BYTES = BN * P_PITCH;
   static constexpr int P_BUFS = N == 64 ? 1 : 2;
-  static constexpr int MISC = 1024 + SOFT / 32 * 256;  // barriers and so on; two rows of 32 floats a softmax warp
+  // barriers and so on; two rows of NC floats a softmax warp; statistics handed over
+  static constexpr int MISC = 1024 + SOFT / 32 * NC * 8 + (TURNS ? 4 * N * 8 : 0);
   static constexpr int Q_BUFS = Q_BYTES > 16384 ? 1 : 2;
   static constexpr int AVAIL = 227 * 1024 - 1024 - Q_BUFS * Q_BYTES - P_BUFS * P_BYTES - MISC;
   static constexpr int FIT = AVAIL / (K_BYTES + V_BYTES);
@@ -60,16 +72,17 @@ struct PagedCfg {
   static constexpr int OFF_P = OFF_Q + Q_BUFS * Q_BYTES;
   static constexpr int OFF_MISC = OFF_P + P_BUFS * P_BYTES;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
-  static constexpr uint32_t TMEM_COLS = 4 * N;
-  static constexpr uint32_t T_S = 0, T_O = 2 * N;      // two tiles of each
+  static constexpr uint32_t TMEM_COLS = TURNS ? 128 : 4 * N;
+  static constexpr uint32_t T_S = 0, T_O = 2 * N;      // S of two tiles; O of two units (of each warpgroup)
+  static constexpr int OS = TURNS ? 2 : 1;
   static_assert(ST >= 2 && SMEM <= 227 * 1024, "shared memory");
 };
 
 // Barriers: rings of K and V, Q of a unit, S and P of a tile, P V done, O of a
-// unit full and read, ring of units.
+// unit full and read, statistics handed over, ring of units.
 enum : int { GB_KF = 0, GB_KE = GB_KF + 6, GB_VF = GB_KE + 6, GB_VE = GB_VF + 6, GB_Q = GB_VE + 6, GB_QE = GB_Q + 2,
              GB_S = GB_QE + 2, GB_P = GB_S + 2, GB_PV = GB_P + 2, GB_O = GB_PV + 2, GB_OE = GB_O + 2,
-             GB_I = GB_OE + 2, GB_IE = GB_I + 4, GB_DRAIN = GB_IE + 4, GB_COUNT = GB_DRAIN + 2 };
+             GB_ST = GB_OE + 2, GB_I = GB_ST + 4, GB_IE = GB_I + 4, GB_DRAIN = GB_IE + 4, GB_COUNT = GB_DRAIN + 2 };
 
 // One unit's part of a run, as the producer tells it.
 struct PagedItem {
@@ -91,6 +104,24 @@ __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// A bounded wait (mbar_wait), of which only the first look is inlined: there are
+// some thirty waits, and the kernel's code has to stay in the instruction cache, whose
+// misses queue behind the keys and values.
+static __device__ __noinline__ bool paged_wait_on(uint32_t bar, uint32_t phase, uint32_t* err,
+                                                  volatile uint32_t* abort, uint32_t site) {
+  return mbar_wait(bar, phase, ErrCtx{err, abort}, site & ~(1u << 31), true, (site >> 31) != 0);
+}
+// By a converged warp; the same result in every lane. sleep: as in mbar_wait.
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t phase, const ErrCtx& e, uint32_t site,
+                                           bool sleep = false) {
+  bool ok = mbar_try_wait(bar, phase);
+  if (!__all_sync(0xffffffffu, ok)) {
+    if (!ok) ok = paged_wait_on(bar, phase, e.err_word, e.abort, site | (sleep ? 1u << 31 : 0u));
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
 }
 
 // Keys of a sequence, and its key tiles [lo, lo + n) that some new token sees.
@@ -123,39 +154,32 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
   int* start = reinterpret_cast<int*>(tmem_slot + 2);              // sequence, place in it
   uint32_t* scan = reinterpret_cast<uint32_t*>(tmem_slot + 4);     // [warps] sums
   int* items = reinterpret_cast<int*>(tmem_slot + 4 + 16);         // ring of 4, 8 words each
-  static_assert((GB_COUNT + 2 + 8 + 16) * 8 <= 1024 && GB_COUNT % 2 == 0, "barrier region");
-  // [softmax warps][32] values of rows. While maxima are exchanged, sMax holds each
+  int* sIds = items + 32;                                          // [producers][32] pages
+  static_assert(GB_COUNT * 8 + 80 + 128 + 256 <= 1024 && GB_COUNT % 2 == 0, "barrier region");
+  // [softmax warps][NC] values of rows. While maxima are exchanged, sMax holds each
   // warp's and sRow is its own; at a unit's end sRow holds each warp's sums and sMax is
   // its own. Between the two uses lies a barrier of the warpgroup.
   float* sMax = reinterpret_cast<float*>(smem + C::OFF_MISC + 1024);
-  float* sRow = sMax + kSoftWarps * 32;
+  float* sRow = sMax + kSoftWarps * NC;
+  float* sStat = sRow + kSoftWarps * NC;  // [4][maximum, sum][N]: statistics of the other warpgroup's tiles
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   // ---- this CTA's run: [lo, hi) of the line of all units
   // thread i has the sequences [i per, (i + 1) per)
   const int per = (p.B + C::THREADS - 1) / C::THREADS;
   const int units = p.H_kv * p.row_blocks;  // of a sequence
-  uint32_t sum = 0;
-  for (int i = tid * per; i < min(p.B, (tid + 1) * per); ++i)
-    sum += static_cast<uint32_t>(paged_span(p, __ldg(p.seqlen + i)).n + kPagedCost);
-  sum *= static_cast<uint32_t>(units);
-  uint32_t upto = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t u = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += u;
-  }
-  if (lane == 31) scan[warp] = upto;
+  const int length0 = tid * per < p.B ? __ldg(p.seqlen + tid * per) : 0;
   if (tid == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+    
+#pragma unroll 1
     for (int i = 0; i < GB_COUNT; ++i) {
       uint32_t n = 1;
-      if (i >= GB_P && i < GB_P + 2) n = kSoftWarps;
-      if (i >= GB_OE && i < GB_OE + 2) n = kSoftWarps;
-      if (i >= GB_IE && i < GB_DRAIN) n = kSoftWarps + 1;
+      if ((i >= GB_P && i < GB_P + 2) || (i >= GB_OE && i < GB_OE + 2)) n = C::TURNS ? kSoftWarps / 2 : kSoftWarps;
+      if (i >= GB_IE && i < GB_DRAIN) n = kSoftWarps + 2;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0u;
@@ -166,9 +190,23 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
     tmem_relinquish();
   }
   // rows of Q that no box fills stay 0
+#pragma unroll 1
   for (int i = tid; i < C::Q_BUFS * C::Q_BYTES / 16; i += C::THREADS)
     reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
+  uint32_t sum = 0;
+  
+#pragma unroll 1
+  for (int i = tid * per; i < min(p.B, (tid + 1) * per); ++i)
+    sum += static_cast<uint32_t>(paged_span(p, i == tid * per ? length0 : __ldg(p.seqlen + i)).n + kPagedCost);
+  sum *= static_cast<uint32_t>(units);
+  uint32_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
+  }
+  if (lane == 31) scan[warp] = upto;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -184,8 +222,10 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
   if (run_lo < run_hi && run_lo >= upto - sum && run_lo < upto) {  // one thread of the CTA
     uint32_t at = run_lo - (upto - sum);
     int i = tid * per;
+#pragma unroll 1
     for (;; ++i) {
-      const uint32_t w = static_cast<uint32_t>(paged_span(p, __ldg(p.seqlen + i)).n + kPagedCost) * units;
+      const int length = i == tid * per ? length0 : __ldg(p.seqlen + i);
+      const uint32_t w = static_cast<uint32_t>(paged_span(p, length).n + kPagedCost) * units;
       if (at < w) break;
       at -= w;
     }
@@ -193,25 +233,34 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
     start[1] = static_cast<int>(at);
   }
   __syncthreads();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const ErrCtx ec{p.err, abort_flag};
   auto next_item = [&](int u, PagedItem* it) -> bool {
-    if (!mbar_wait_w(bar(GB_I + (u & 3)), (u >> 2) & 1, ec, kSiteFwdSoftmax)) return false;
+    if (!paged_wait(bar(GB_I + (u & 3)), (u >> 2) & 1, ec, kSiteFwdSoftmax)) return false;
     const int4 a = *reinterpret_cast<const int4*>(items + (u & 3) * 8);
     const int4 b = *reinterpret_cast<const int4*>(items + (u & 3) * 8 + 4);
-    *it = PagedItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    auto one = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    *it = PagedItem{one(a.x), one(a.y), one(a.z), one(a.w), one(b.x), one(b.y), one(b.z)};
     return true;
   };
 
-  if (warp == kSoftWarps) {
-    // ------------------------------------------------------------ producer
-    int nk = 0, nv = 0, nu = 0, nq = 0;  // tiles of K and V, items, items with keys so far
+  if (warp == kSoftWarps || warp == kSoftWarps + 2) {
+    // ----------------------------------------------------------- producers
+    const bool keys = warp == kSoftWarps;
+    const int width = keys ? DQK / 64 : DV / 64;  // 64-column chunks
+    const uint32_t ring = keys ? sK : sV, stage_bytes = keys ? C::K_BYTES : C::V_BYTES;
+    const int full = keys ? GB_KF : GB_VF, empty = keys ? GB_KE : GB_VE;
+    const CUtensorMap* map = keys ? &tmK : &tmV;
+    auto free_of = [&](int i, int round) {  // the round's use of barrier i's buffer may begin
+      return paged_wait(bar(i), (round & 1) ^ 1, ec, kSiteFwdLoad, true);
+    };
+    int nt = 0, nu = 0, nq = 0;  // tiles copied, items told, items with keys so far
+    int s = 0, round = 0;        // stage of the ring, and its uses
     bool ok = true;
     int4 runs = make_int4(0, 0, 0, 0);
     auto tell = [&](const PagedItem& it) -> bool {
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait(bar(GB_IE + (nu & 3)), ((nu >> 2) & 1) ^ 1, ec, kSiteFwdLoad, true, true)))
-        return false;
+      if (!keys) return true;
+      if (!free_of(GB_IE + (nu & 3), nu >> 2)) return false;
       if (lane == 0) {
         *reinterpret_cast<int4*>(items + (nu & 3) * 8) = make_int4(it.n, it.b, it.hk, it.rb);
         *reinterpret_cast<int4*>(items + (nu & 3) * 8 + 4) = make_int4(it.k0, it.len, it.slot, 0);
@@ -221,12 +270,32 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
       ++nu;
       return true;
     };
+    // lengths of 32 sequences from l0 on, a lane each, and of the 32 after them
+    int l0 = start[0];
     uint32_t left = run_hi - run_lo;
-    int i = 0, unit = 0, pos = 0;
-    PagedSpan sp{0, 0, 0};
+    auto length = [&](int i) { return i < p.B ? __ldg(p.seqlen + i) : 0; };
+    int lens = left > 0 ? length(l0 + lane) : 0, lens_ahead = left > 0 ? length(l0 + 32 + lane) : 0;
+    auto span_of = [&](int i) {  // i in [l0, l0 + 64)
+      const int near = __shfl_sync(0xffffffffu, lens, (i - l0) & 31), far = __shfl_sync(0xffffffffu, lens_ahead, (i - l0) & 31);
+      return paged_span(p, i - l0 < 32 ? near : far);
+    };
+    // A tile's copies are boxes of a page, of `box` keys each. Lane l has the page of
+    // box ib + l of sequence is (in shared memory too, for the lane that copies), and of
+    // the batch of boxes that is wanted next.
+    const int per_tile = BN >> p.box_shift;
+    int is = -1, ib = 0, ids = 0, as = -1, ab = 0, ids_ahead = 0;
+    int* own_ids = sIds + (keys ? 0 : 32);
+    auto pages_of = [&](int i, int len, int b0) {
+      const int key = (b0 + lane) << p.box_shift;
+      const int id = key < len ? __ldg(p.table + i * p.table_stride + (key >> p.page_shift)) : 0;
+      // (the first page behind the pool reads as zeros)
+      return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages) ? id : p.n_pages;
+    };
+    int i = l0, unit = 0, pos = 0;
+    PagedSpan sp{0, 0, 0}, sp_next{0, 0, 0};
     if (left > 0) {
-      i = start[0];
-      sp = paged_span(p, __ldg(p.seqlen + i));
+      sp = span_of(i);
+      sp_next = span_of(i + 1);
       const int w = sp.n + kPagedCost;
       unit = start[1] / w;
       pos = start[1] - unit * w;
@@ -256,63 +325,66 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
         }
         if (!(ok = tell(it))) break;
         if (it.n > 0) {
-          const int qb = nq % C::Q_BUFS;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(GB_QE + qb), ((nq / C::Q_BUFS) & 1) ^ 1, ec, kSiteFwdLoad, true,
-                                                       true))))
-            break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(GB_Q + qb), (DQK / 64) * p.q_box);
+          if (keys) {
+            const int qb = nq % C::Q_BUFS;
+            if (!(ok = free_of(GB_QE + qb, nq / C::Q_BUFS))) break;
+            if (elect_one_sync()) {
+              mbar_arrive_expect_tx(bar(GB_Q + qb), (DQK / 64) * p.q_box);
 #pragma unroll
-            for (int c = 0; c < DQK / 64; ++c)
-              tma_load_4d(sQ + qb * C::Q_BYTES + c * N * 128, &tmQ, bar(GB_Q + qb), c * 64, it.rb * N, it.b, it.hk);
+              for (int c = 0; c < DQK / 64; ++c)
+                tma_load_4d(sQ + qb * C::Q_BYTES + c * N * 128, &tmQ, bar(GB_Q + qb), c * 64, it.rb * N, it.b, it.hk);
+            }
+            __syncwarp();
+            ++nq;
           }
-          ++nq;
-          // Keys that some token sees: [seen, len). A tile's copies are boxes of a page,
-          // of `box` keys each; lane l has the page of box b0 + l.
+          // boxes with a key that some token sees: [first, end)
           const int seen = p.left < 0 ? 0 : max(0, sp.len - p.s_q - p.left);
-          const int per_tile = BN >> p.box_shift;
-          const int* row = p.table + i * p.table_stride;
-          auto page_of = [&](int box) {
-            const int key = box << p.box_shift;
-            const int id = key < sp.len ? __ldg(row + (key >> p.page_shift)) : 0;
-            // (the first page behind the pool reads as zeros)
-            return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages) ? id : p.n_pages;
-          };
-          int b0 = it.k0 * per_tile;
-          int ids = page_of(b0 + lane), ahead = page_of(b0 + 32 + lane);
+          const int first = seen >> p.box_shift, end = (sp.len + p.box - 1) >> p.box_shift;
+          const bool again = unit + 1 < units;  // the next unit is of the same sequence
           for (int j = 0; j < it.n; ++j) {
             const int box0 = (it.k0 + j) * per_tile;
-            if (box0 - b0 == 32) {
-              b0 = box0;
-              ids = ahead;
-              ahead = page_of(b0 + 32 + lane);
+            if (j == 0 || box0 - ib == 32) {  // another batch of pages
+              const int want = box0;
+              if (is != i || ib != want) {
+                ids = as == i && ab == want ? ids_ahead : pages_of(i, sp.len, want);
+                is = i;
+                ib = want;
+                own_ids[lane] = ids;
+                __syncwarp();
+              }
+              // ... and the one after it: of this unit, of the next one of the
+              // sequence, or of the next sequence
+              if ((it.k0 + it.n) * per_tile > want + 32) {
+                as = i, ab = want + 32;
+                ids_ahead = pages_of(i, sp.len, ab);
+              } else if (again && sp.lo * per_tile != want) {
+                as = i, ab = sp.lo * per_tile;
+                ids_ahead = pages_of(i, sp.len, ab);
+              } else if (i + 1 < p.B && (as != i + 1 || ab != sp_next.lo * per_tile)) {
+                as = i + 1, ab = sp_next.lo * per_tile;
+                ids_ahead = pages_of(i + 1, sp_next.len, ab);
+              }
             }
-            const int s = nk % ST;
-            const uint32_t ph = static_cast<uint32_t>(nk / ST) & 1u;
-            // boxes of the tile with a visible key
-            const int lo = max(box0, seen >> p.box_shift);
-            const int hi = min(box0 + per_tile, (sp.len + p.box - 1) >> p.box_shift);
-            const uint32_t bytes = static_cast<uint32_t>(hi - lo) * static_cast<uint32_t>(p.box) * 128u;
-            // lane l copies column chunk l / per_tile (and further ones) of box l % per_tile
-            const int my_box = box0 + (lane & (per_tile - 1));
-            const int pg = __shfl_sync(0xffffffffu, ids, my_box - b0);
-            const bool mine = my_box >= lo && my_box < hi;
-            const int key = my_box << p.box_shift, in_page = key & ((1 << p.page_shift) - 1);
-            const uint32_t dst = static_cast<uint32_t>(key - box0 * p.box) * 128u;
-            auto copy = [&](int chunks, uint32_t base, const CUtensorMap* m, uint32_t b) {
-              if (lane == 0) mbar_arrive_expect_tx(b, bytes * chunks);
-              __syncwarp();
-              if (mine)
-                for (int c = lane / per_tile; c < chunks; c += 32 / per_tile)
-                  tma_load_4d(base + c * BN * 128 + dst, m, b, c * 64, in_page, it.hk, pg);
-              __syncwarp();
-            };
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(GB_KE + s), ph ^ 1, ec, kSiteFwdLoad, true, true)))) break;
-            copy(DQK / 64, sK + s * C::K_BYTES, &tmK, bar(GB_KF + s));
-            ++nk;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(GB_VE + s), ph ^ 1, ec, kSiteFwdLoad, true, true)))) break;
-            copy(DV / 64, sV + s * C::V_BYTES, &tmV, bar(GB_VF + s));
-            ++nv;
+            if (!(ok = free_of(empty + s, round))) break;
+            const int lo = max(box0, first), hi = min(box0 + per_tile, end);
+            if (elect_one_sync()) {
+              const uint32_t b = bar(full + s), rows = static_cast<uint32_t>(p.box) * 128u;  // bytes of a box
+              mbar_arrive_expect_tx(b, static_cast<uint32_t>(hi - lo) * rows * width);
+              uint32_t dst = ring + s * stage_bytes + static_cast<uint32_t>(lo - box0) * rows;
+#pragma unroll 1
+              for (int x = lo; x < hi; ++x, dst += rows) {
+                const int pg = own_ids[x - ib], in_page = (x << p.box_shift) & ((1 << p.page_shift) - 1);
+#pragma unroll
+                for (int c = 0; c < DQK / 64; ++c)
+                  if (c < width) tma_load_4d(dst + c * BN * 128, map, b, c * 64, in_page, it.hk, pg);
+              }
+            }
+            __syncwarp();
+            ++nt;
+            if (++s == ST) {
+              s = 0;
+              ++round;
+            }
           }
           if (!ok) break;
         }
@@ -322,100 +394,156 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
       if (++unit == units && left > 0) {
         unit = 0;
         ++i;
-        sp = paged_span(p, __ldg(p.seqlen + i));
+        if (i - l0 == 32) {
+          l0 = i;
+          lens = lens_ahead;
+          lens_ahead = length(l0 + 32 + lane);
+        }
+        sp = sp_next;
+        sp_next = span_of(i + 1);
       }
     }
     if (ok) tell(PagedItem{-1, 0, 0, 0, 0, 0, 0});
-    if (lane == 0) p.runs[blockIdx.x] = runs;
+    if (keys && lane == 0) p.runs[blockIdx.x] = runs;
     // Every copy issued must land before the CTA can retire; on the healthy path they
     // did long ago.
     __syncwarp();
     if (*abort_flag) {
+      
+#pragma unroll 1
       for (int b = 0; b < C::Q_BUFS; ++b)
         if (nq > b) mbar_wait(bar(GB_Q + b), ((nq - 1 - b) / C::Q_BUFS) & 1, ec, kSiteDrain, false);
-      for (int s = 0; s < ST; ++s) {
-        if (nk > s) mbar_wait(bar(GB_KF + s), ((nk - 1 - s) / ST) & 1, ec, kSiteDrain, false);
-        if (nv > s) mbar_wait(bar(GB_VF + s), ((nv - 1 - s) / ST) & 1, ec, kSiteDrain, false);
-      }
+#pragma unroll 1
+      for (int s = 0; s < ST; ++s)
+        if (nt > s) mbar_wait(bar(full + s), ((nt - 1 - s) / ST) & 1, ec, kSiteDrain, false);
     }
   } else if (warp == kSoftWarps + 1) {
-    // ---------------------------------------------------------- MMA issuer
+    // ------------------------------------------------- S^T = K Q^T
     constexpr uint32_t kIdS = idesc_f16(128, N, BF16, false, false);
-    constexpr uint32_t kIdO = idesc_f16(DV, N, BF16, true, true);
-    const uint64_t dK0 = sdesc_sw128(sK, 16, 1024);
-    const uint64_t dQ0 = sdesc_sw128(sQ, 16, 1024);
-    const uint64_t dV0 = sdesc_sw128(sV, BN * 128, 1024);
-    const uint64_t dP0 = paged_desc_p(sP, C::P_PITCH);
-    int u = 0, g = 0, q = 0;  // item, key tile, item with keys
+    const uint64_t dK0 = sdesc_sw128(sK, 16, 1024), dQ0 = sdesc_sw128(sQ, 16, 1024);
+    int g = 0, q = 0, s = 0;  // tile, item with keys, stage
+    uint32_t ph = 0;          // the stage's phase
     bool ok = true;
-    // S of tile g, the j-th of an item of n
-    auto issue_s = [&](int gs, int qs, bool first, bool last) -> bool {
-      if (first && !mbar_wait_w(bar(GB_Q + qs % C::Q_BUFS), (qs / C::Q_BUFS) & 1, ec, kSiteFwdMma)) return false;
-      if (!mbar_wait_w(bar(GB_KF + gs % ST), (gs / ST) & 1, ec, kSiteFwdMma)) return false;
-      tc_fence_after();
-      const uint64_t dK = opaque_u64(desc_adv(dK0, (gs % ST) * C::K_BYTES));
-      const uint64_t dQ = opaque_u64(desc_adv(dQ0, (qs % C::Q_BUFS) * C::Q_BYTES));
+    PagedItem it;
+    for (int u = 0; (ok = next_item(u, &it)); ++u) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(GB_IE + (u & 3)));
+      if (it.n < 0) break;
+      if (it.n == 0) continue;
+      const int qb = q % C::Q_BUFS;
+      if (!(ok = paged_wait(bar(GB_Q + qb), (q / C::Q_BUFS) & 1, ec, kSiteFwdMma))) break;
+      const uint64_t dQ = desc_adv(dQ0, qb * C::Q_BYTES);
+      for (int j = 0; j < it.n; ++j, ++g) {
+        // S's buffer: P of the tile before the last one, formed from it, is there
+        if (!(ok = paged_wait(bar(GB_P + (g & 1)), ((g >> 1) & 1) ^ 1, ec, kSiteFwdMma))) break;
+        if (!(ok = paged_wait(bar(GB_KF + s), ph, ec, kSiteFwdMma))) break;
+        tc_fence_after();
+        const uint64_t dK = desc_adv(dK0, s * C::K_BYTES);
+        if (elect_one_sync()) {
 #pragma unroll
-      for (int kk = 0; kk < DQK / 16; ++kk)
-        umma_ss_w(tbase + C::T_S + N * (gs & 1), desc_adv(dK, (kk >> 2) * (BN * 128) + (kk & 3) * 32),
-                  desc_adv(dQ, (kk >> 2) * (N * 128) + (kk & 3) * 32), kIdS, kk > 0);
-      umma_commit_w(bar(GB_S + (gs & 1)));
-      umma_commit_w(bar(GB_KE + gs % ST));
-      if (last) umma_commit_w(bar(GB_QE + qs % C::Q_BUFS));
-      return true;
-    };
-    auto issue_pv = [&](int gv, int qv, bool first, bool last) -> bool {
-      const int ob = qv & 1;
-      // O's buffer has been read (of the item before the last one)
-      if (first && !mbar_wait_w(bar(GB_OE + ob), ((qv >> 1) & 1) ^ 1, ec, kSiteFwdMma)) return false;
-      if (!mbar_wait_w(bar(GB_VF + gv % ST), (gv / ST) & 1, ec, kSiteFwdMma)) return false;
-      if (!mbar_wait_w(bar(GB_P + (gv & 1)), (gv >> 1) & 1, ec, kSiteFwdMma)) return false;
-      tc_fence_after();
-      const uint64_t dV = opaque_u64(desc_adv(dV0, (gv % ST) * C::V_BYTES));
-      const uint64_t dP = opaque_u64(desc_adv(dP0, (C::P_BUFS == 2 ? (gv & 1) : 0) * C::P_BYTES));
-#pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk)
-        umma_ss_w(tbase + C::T_O + N * ob, desc_adv(dV, kk * 2048), desc_adv(dP, kk * 16 * C::P_PITCH), kIdO,
-                  !first || kk > 0);
-      umma_commit_w(bar(GB_VE + gv % ST));
-      umma_commit_w(bar(GB_PV + (gv & 1)));
-      if (last) umma_commit_w(bar(GB_O + ob));
-      return true;
-    };
-    for (;; ++u) {
-      PagedItem it;
-      if (!(ok = next_item(u, &it))) break;
-      if (it.n >= 0) {
-        if (it.n > 0) ok = issue_s(g, q, true, it.n == 1);
-        for (int j = 0; ok && j < it.n; ++j, ++g) {
-          // the next tile's S first, if its keys are there: it runs while the softmax does
-          const bool more = j + 1 < it.n;
-          const bool early =
-              more && __all_sync(0xffffffffu, mbar_try_wait(bar(GB_KF + (g + 1) % ST), ((g + 1) / ST) & 1));
-          if (early) ok = issue_s(g + 1, q, false, j + 2 == it.n);
-          if (ok) ok = issue_pv(g, q, j == 0, !more);
-          if (ok && more && !early) ok = issue_s(g + 1, q, false, j + 2 == it.n);
+          for (int kk = 0; kk < DQK / 16; ++kk)
+            umma_ss(tbase + C::T_S + N * (g & 1), desc_adv(dK, (kk >> 2) * (BN * 128) + (kk & 3) * 32),
+                    desc_adv(dQ, (kk >> 2) * (N * 128) + (kk & 3) * 32), kIdS, kk > 0);
+          umma_commit(bar(GB_S + (g & 1)));
+          umma_commit(bar(GB_KE + s));
+          if (j + 1 == it.n) umma_commit(bar(GB_QE + qb));
         }
-        if (it.n > 0) ++q;
+        __syncwarp();
+        if (++s == ST) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
       if (!ok) break;
-      if (lane == 0) mbar_arrive(bar(GB_IE + (u & 3)));
-      __syncwarp();
-      if (it.n < 0) break;
+      ++q;
     }
     umma_commit_w(bar(GB_DRAIN));
     mbar_wait(bar(GB_DRAIN), 0, ec, kSiteDrain, false);
+  } else if (warp == kSoftWarps + 3) {
+    // ------------------------------------------------- O^T = V^T P^T
+    constexpr uint32_t kIdO = idesc_f16(DV, N, BF16, true, true);
+    const uint64_t dV0 = sdesc_sw128(sV, BN * 128, 1024), dP0 = paged_desc_p(sP, C::P_PITCH);
+    int g = 0, q = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    PagedItem it;
+    for (int u = 0; (ok = next_item(u, &it)); ++u) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(GB_IE + (u & 3)));
+      if (it.n < 0) break;
+      if (it.n == 0) continue;
+      const int ob = q & 1;
+      // O's buffer has been read (of the item before the last one)
+      if (!(ok = paged_wait(bar(GB_OE + ob), ((q >> 1) & 1) ^ 1, ec, kSiteFwdMma))) break;
+      const int seen = p.left < 0 ? 0 : max(0, it.len - p.s_q - p.left);
+      for (int j = 0; j < it.n; ++j, ++g) {
+        if (!(ok = paged_wait(bar(GB_VF + s), ph, ec, kSiteFwdMma))) break;
+        // Keys [lo, hi) of the tile are seen by some row. Only the steps of 16 keys that
+        // hold one of them are multiplied; what such a step has besides (the page's rows
+        // behind the last key, say) may be anything: its values are zeroed first.
+        const int key0 = (it.k0 + j) * BN, lo = max(0, seen - key0), hi = min(BN, it.len - key0);
+        const int k0 = lo / 16, k1 = (hi + 15) / 16;
+        if (((lo | hi) & 15) != 0) {
+          uint8_t* v = smem + C::OFF_V + s * C::V_BYTES;
+          const int front = lo & 15, rows = front + (-hi & 15);
+            #pragma unroll 1
+#pragma unroll 1
+          for (int e = lane; e < rows * 8; e += 32) {
+            const int r = e / 8 < front ? lo - front + e / 8 : hi + e / 8 - front;
+#pragma unroll
+            for (int c = 0; c < DV / 64; ++c)
+              *reinterpret_cast<uint4*>(v + c * BN * 128 + r * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!(ok = paged_wait(bar(GB_P + (g & 1)), (g >> 1) & 1, ec, kSiteFwdMma))) break;
+        tc_fence_after();
+        const uint64_t dV = desc_adv(dV0, s * C::V_BYTES);
+        const uint64_t dP = desc_adv(dP0, (C::P_BUFS == 2 ? (g & 1) : 0) * C::P_BYTES);
+        const uint32_t dO = tbase + C::T_O + N * (C::TURNS ? 2 * ob + (g & 1) : ob);
+        const bool first = j < C::OS;  // of the tiles that this O sums
+        if (elect_one_sync()) {
+          if (k1 - k0 == BN / 16) {
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              umma_ss(dO, desc_adv(dV, kk * 2048), desc_adv(dP, kk * 16 * C::P_PITCH), kIdO, !first || kk > 0);
+          } else {
+#pragma unroll 1
+            for (int kk = k0; kk < k1; ++kk)
+              umma_ss(dO, desc_adv(dV, kk * 2048), desc_adv(dP, kk * 16 * C::P_PITCH), kIdO, !first || kk > k0);
+          }
+          umma_commit(bar(GB_PV + (g & 1)));
+          umma_commit(bar(GB_VE + s));
+          if (j + 1 == it.n) umma_commit(bar(GB_O + ob));
+        }
+        __syncwarp();
+        if (++s == ST) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      ++q;
+    }
+    umma_commit_w(bar(GB_DRAIN + 1));
+    mbar_wait(bar(GB_DRAIN + 1), 0, ec, kSiteDrain, false);
   } else {
     // -------------------------------------------------------------- softmax
     const int t = warp >> 2, w4 = warp & 3;
-    const int col0 = t * NC;            // first row of this warpgroup
-    const int own_key = w4 * 32 + lane;  // this thread's key of a tile
-    const uint32_t tS = tbase + C::T_S + col0 + (static_cast<uint32_t>(w4 * 32) << 16);
-    const uint32_t tO = tbase + C::T_O + col0 + (static_cast<uint32_t>(w4 * 32) << 16);
-    float* gMax = sMax + t * 128;
-    float* gRow = sRow + t * 128;
-    float* wMax = gMax + w4 * 32;
-    float* wRow = gRow + w4 * 32;
+    const int col0 = C::TURNS ? 0 : t * NC;  // first row of this warpgroup
+    const int own_key = w4 * 32 + lane;       // this thread's key of a tile
+    const uint32_t own_lanes = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t tS = tbase + C::T_S + col0 + own_lanes;
+    // O of the item's tiles (turns: those of warpgroup w)
+    auto tO = [&](int q, int w) {
+      return tbase + C::T_O + N * (C::TURNS ? 2 * (q & 1) + w : (q & 1)) + col0 + own_lanes;
+    };
+    float* gMax = sMax + t * 4 * NC;
+    float* gRow = sRow + t * 4 * NC;
+    float* wMax = gMax + w4 * NC;
+    float* wRow = gRow + w4 * NC;
+    const int own_row = lane & (NC - 1);
     const float sl2 = p.scale_log2;
     const float hide = sl2 < 0.f ? -SDPA_NEG_INF : SDPA_NEG_INF;  // masked raw score
     // 16-byte chunk of a key's row of P^T, as the swizzle has it
@@ -433,7 +561,6 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]);
       }
-      tmem_wait_ld();
     };
     auto spread = [&](float* own, float v, float (&x)[NC]) {  // lane e's value of row e to all lanes
       __syncwarp();
@@ -445,8 +572,15 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
         x[e] = f.x, x[e + 1] = f.y, x[e + 2] = f.z, x[e + 3] = f.w;
       }
     };
+    // P = 2^(y - m) of the log2 scores y. m need not be the row's maximum: what P is
+    // rounded to has to hold it with all its bits, and fp32 the sums. fp16 wants m
+    // within 2^8; bf16 has fp32's exponents, and 2^60 either way is fine, so it begins
+    // with m = 0 where all scores that a row sees of its first tile lie within that,
+    // without asking for their maximum, which takes the warpgroup longer than the
+    // softmax of the tile.
+    constexpr float kFar = BF16 ? 60.f : 8.f;
     constexpr float kNone = 1e30f;  // -m of a row without a score: any score then grows it
-    int u = 0, g = 0, q = 0;
+    int u = 0, g0 = 0, q = 0, pairs = 0;  // item, its first tile, items with keys, items of both warpgroups
     bool ok = true, left_all = false;
     PagedItem it;
     for (; (ok = next_item(u, &it)) && it.n >= 0; ++u) {
@@ -454,7 +588,9 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
       const int live = min(NC, p.R - base);
       const int64_t row0 = (static_cast<int64_t>(it.b) * p.H_kv + it.hk) * p.R + base;
       if (it.n == 0) {  // a sequence without a key
-        for (int e = w4; e < live; e += 4) {
+#pragma unroll 1
+        for (int e = C::TURNS ? warp : w4; e < live; e += C::TURNS ? 8 : 4) {
+#pragma unroll 1
           for (int d = lane; d < DV / 2; d += 32) static_cast<uint32_t*>(p.o)[(row0 + e) * (DV / 2) + d] = 0u;
           if (lane == 0) p.lse[row0 + e] = SDPA_NEG_INF;
         }
@@ -463,72 +599,89 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
         continue;
       }
       const int last0 = it.len - p.s_q;  // last key of token 0
-      const int seen = p.left < 0 ? 0 : max(0, last0 - p.left);  // first key of token 0
-      float nm[NC], l[NC], m = SDPA_NEG_INF;  // (m: row `lane`)
+      float nm[NC], l[NC], m = BF16 ? 0.f : SDPA_NEG_INF;  // -m and sums of this key's; m: of row `own_row`
 #pragma unroll
       for (int e = 0; e < NC; ++e) {
-        nm[e] = kNone;
+        nm[e] = BF16 ? 0.f : kNone;
         l[e] = 0.f;
       }
-      for (int j = 0; j < it.n; ++j, ++g) {
-        const int key0 = (it.k0 + j) * BN, key = key0 + own_key;
-        if (ok) ok = mbar_wait(bar(GB_S + (g & 1)), (g >> 1) & 1, ec, kSiteFwdSoftmax);
-        ok = __all_sync(0xffffffffu, ok);
+      const int j0 = C::TURNS ? (g0 ^ t) & 1 : 0;
+      for (int j = j0; j < it.n; j += C::OS) {
+        const int g = g0 + j, key0 = (it.k0 + j) * BN, key = key0 + own_key;
+        const bool first = j == j0;
+        if (ok) ok = paged_wait(bar(GB_S + (g & 1)), (g >> 1) & 1, ec, kSiteFwdSoftmax);
         tc_fence_after();
         float x[NC];
         load(tS + N * (g & 1), x);
+        tmem_wait_ld();
         if (p.capped) {
 #pragma unroll
           for (int e = 0; e < NC; ++e) x[e] = rcp(1.f + ex2(x[e] * p.cap_in));
         }
-        if (key0 + BN - 1 > last0 || (p.left >= 0 && key0 < last0 + p.s_q - 1 - p.left)) {
+        const bool hidden = key0 + BN - 1 > last0 || (p.left >= 0 && key0 < last0 + p.s_q - 1 - p.left);
+        bool out = false;  // a key that no row sees
+        if (hidden) {
           int tok = base % p.s_q;
+          out = true;
 #pragma unroll
           for (int e = 0; e < NC; ++e) {
-            if (key > last0 + tok || (p.left >= 0 && key < last0 + tok - p.left)) x[e] = hide;
+            if (key > last0 + tok || (p.left >= 0 && key < last0 + tok - p.left))
+              x[e] = hide;
+            else
+              out = false;
             tok = tok + 1 == p.s_q ? 0 : tok + 1;
           }
         }
-        float most = SDPA_NEG_INF;
+        float most = SDPA_NEG_INF, least = -SDPA_NEG_INF;
 #pragma unroll
-        for (int e = 0; e < NC; ++e) most = fmaxf(most, fmaf(x[e], sl2, nm[e]));
-        if (!vote(ok && !(most > 8.f))) {
-          // ---- some row's maximum has grown: exchange them
+        for (int e = 0; e < NC; ++e) {
+          const float y = fmaf(x[e], sl2, nm[e]);
+          most = fmaxf(most, y);
+          if constexpr (BF16) least = fminf(least, y);
+        }
+        // (rows of several tokens see a tile's keys only in part: such a tile says nothing of
+        // the rows that see none of it)
+        bool fine = most <= kFar;
+        if (first) fine = fine && BF16 && (out || least >= -kFar) && (p.s_q == 1 || !hidden);
+        if (!vote(ok && fine)) {
+          // ---- the rows' maxima, of all keys of the tile
           float mine = SDPA_NEG_INF;
 #pragma unroll
           for (int e = 0; e < NC; ++e) {
             const float r = warp_max(x[e] * sl2);
-            if (lane == e) mine = r;
+            if (own_row == e) mine = r;
           }
-          wMax[lane] = mine;
+          if (lane < NC) wMax[lane] = mine;
           if (!vote(ok)) {
             left_all = true;
             break;
           }
-          const int e0 = lane & (NC - 1);
-          const float mx = fmaxf(fmaxf(gMax[e0], gMax[32 + e0]), fmaxf(gMax[64 + e0], gMax[96 + e0]));
+          const float mx = fmaxf(fmaxf(gMax[own_row], gMax[NC + own_row]),
+                                 fmaxf(gMax[2 * NC + own_row], gMax[3 * NC + own_row]));
+          if (first) m = SDPA_NEG_INF;
           float alpha = 1.f;
-          if (mx > m + 8.f) {
+          if (mx > m + kFar) {
             alpha = ex2(m - mx);
             m = mx;
           }
           spread(wRow, m == SDPA_NEG_INF ? kNone : -m, nm);
-          float al[NC];
-          spread(wRow, alpha, al);
-#pragma unroll
-          for (int e = 0; e < NC; ++e) l[e] *= al[e];
-          if (j > 0) {
-            if (ok) ok = mbar_wait(bar(GB_PV + ((g - 1) & 1)), ((g - 1) >> 1) & 1, ec, kSiteFwdSoftmax);
-            ok = __all_sync(0xffffffffu, ok);
+          if (!first) {
+            float al[NC], o[NC];
+            spread(wRow, alpha, al);
+            // (the product of the warpgroup's tile before this one is done)
+            const int before = g - C::OS;
+            if (ok) ok = paged_wait(bar(GB_PV + (before & 1)), (before >> 1) & 1, ec, kSiteFwdSoftmax);
             tc_fence_after();
-            float o[NC];
-            load(tO + N * (q & 1), o);
+            load(tO(q, t), o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < NC; ++e) l[e] *= al[e];
 #pragma unroll
             for (int e0 = 0; e0 < NC; e0 += 16) {
               uint32_t r[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e0 + e] * al[e0 + e]);
-              tmem_st16(tO + N * (q & 1) + e0, r);
+              tmem_st16(tO(q, t) + e0, r);
             }
             tmem_wait_st();
           }
@@ -541,9 +694,9 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
         // P's buffer: the product that read it last is done
         if (ok) {
           if constexpr (C::P_BUFS == 2)
-            ok = mbar_wait(bar(GB_PV + (g & 1)), ((g >> 1) & 1) ^ 1, ec, kSiteFwdSoftmax);
+            ok = paged_wait(bar(GB_PV + (g & 1)), ((g >> 1) & 1) ^ 1, ec, kSiteFwdSoftmax);
           else if (g > 0)
-            ok = mbar_wait(bar(GB_PV + ((g - 1) & 1)), ((g - 1) >> 1) & 1, ec, kSiteFwdSoftmax);
+            ok = paged_wait(bar(GB_PV + ((g - 1) & 1)), ((g - 1) >> 1) & 1, ec, kSiteFwdSoftmax);
         }
         uint8_t* to = own_p + (C::P_BUFS == 2 ? (g & 1) : 0) * C::P_BYTES;
 #pragma unroll
@@ -551,87 +704,109 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
           *reinterpret_cast<uint4*>(to + (((col0 + e) / 8) ^ flip) * 16) =
               make_uint4(pack2<BF16>(x[e], x[e + 1]), pack2<BF16>(x[e + 2], x[e + 3]),
                          pack2<BF16>(x[e + 4], x[e + 5]), pack2<BF16>(x[e + 6], x[e + 7]));
-        // values of keys that no row sees
-        const int front = min(BN, max(0, seen - key0)), back = min(BN, it.len - key0);
-        if (front > 0 || back < BN) {
-          if (ok) ok = mbar_wait(bar(GB_VF + g % ST), (g / ST) & 1, ec, kSiteFwdSoftmax);
-          uint8_t* v = smem + C::OFF_V + (g % ST) * C::V_BYTES;
-          for (int e = tid; e < (front + BN - back) * 8; e += C::SOFT) {
-            const int r = e / 8 < front ? e / 8 : e / 8 - front + back;
-#pragma unroll
-            for (int c = 0; c < DV / 64; ++c)
-              *reinterpret_cast<uint4*>(v + c * BN * 128 + r * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-        ok = __all_sync(0xffffffffu, ok);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(GB_P + (g & 1)));
       }
       if (left_all) break;
-      // ---- the unit's rows: O / l, and the log of the sum of exponentials
-      // sums over the warp's keys: lane e gets row e's
+      const bool both = C::TURNS && it.n > 1;
+      const bool ends = !C::TURNS || ((g0 + it.n - 1) & 1) == t;  // this warpgroup writes the rows
+      if (j0 < it.n) {
+        // ---- sums over the warp's keys: lane e gets row e's
 #pragma unroll
-      for (int o = NC / 2; o > 0; o >>= 1) {
-        const bool hi = (lane & o) != 0;
+        for (int o = NC / 2; o > 0; o >>= 1) {
+          const bool hi = (lane & o) != 0;
 #pragma unroll
-        for (int e = 0; e < o; ++e) {
-          const float send = hi ? l[e] : l[e + o], keep = hi ? l[e + o] : l[e];
-          l[e] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          for (int e = 0; e < o; ++e) {
+            const float send = hi ? l[e] : l[e + o], keep = hi ? l[e + o] : l[e];
+            l[e] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        }
+        if constexpr (NC == 16) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+        __syncwarp();
+        if (lane < NC) wRow[lane] = l[0];
+        if (!vote(ok)) {
+          vote(false);
+          left_all = true;
+          break;
+        }
+        float sum_l = (gRow[own_row] + gRow[NC + own_row]) + (gRow[2 * NC + own_row] + gRow[3 * NC + own_row]);
+        float* stat = sStat + (pairs & 3) * 2 * N;
+        if (ends) {
+          // ---- the unit's rows: O / l, and the log of the sum of exponentials
+          float c_own = 1.f, c_other = 0.f;
+          if (both) {  // join the other warpgroup's tiles
+            ok = paged_wait(bar(GB_ST + (pairs & 3)), (pairs >> 2) & 1, ec, kSiteFwdSoftmax);
+            const float m2 = stat[own_row], l2 = stat[N + own_row], top = fmaxf(m, m2);
+            const float b = top == SDPA_NEG_INF ? 0.f : top;
+            c_own = ex2(m - b);
+            c_other = ex2(m2 - b);
+            sum_l = sum_l * c_own + l2 * c_other;
+            m = top;
+          }
+          const float inv = sum_l == 0.f ? 0.f : 1.f / sum_l;
+          float c[NC], c2[NC], o[NC];
+          spread(wMax, c_own * inv, c);
+          if (both) spread(wMax, c_other * inv, c2);
+          const float log_l = sum_l == 0.f ? SDPA_NEG_INF : m + __log2f(sum_l) + p.lse_shift;
+          if (w4 == 0 && lane < live) {
+            if (it.slot < 0)
+              p.lse[row0 + lane] = log_l * kLn2;
+            else
+              p.part_lse[it.slot * N + col0 + lane] = log_l;
+          }
+          ok = paged_wait(bar(GB_O + (q & 1)), (q >> 1) & 1, ec, kSiteFwdSoftmax) && ok;
+          tc_fence_after();
+          load(tO(q, t), o);
+          if (both) {
+            float o2[NC];
+            load(tO(q, t ^ 1), o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < NC; ++e)
+              o[e] = (c[e] == 0.f ? 0.f : o[e] * c[e]) + (c2[e] == 0.f ? 0.f : o2[e] * c2[e]);
+          } else {
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < NC; ++e) o[e] = c[e] == 0.f ? 0.f : o[e] * c[e];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(GB_OE + (q & 1)));
+          // (64 value columns: the product's rows lie on each warp's first 16 lanes)
+          const int d = DV == 128 ? own_key : w4 * 16 + lane;
+          const bool has = DV == 128 || lane < 16;
+          if (it.slot >= 0) {
+            float* dst = p.part + static_cast<int64_t>(it.slot * N + col0) * DV + d;
+#pragma unroll
+            for (int e = 0; e < NC; ++e)
+              if (has && e < live) dst[e * DV] = o[e];
+          } else {
+            // two rows at a time: neighbouring lanes swap, and store two columns of a row each
+            const bool odd = (lane & 1) != 0;
+            uint32_t* dst = static_cast<uint32_t*>(p.o) + row0 * (DV / 2) + d / 2;
+#pragma unroll
+            for (int e = 0; e < NC; e += 2) {
+              const float other = __shfl_xor_sync(0xffffffffu, odd ? o[e] : o[e + 1], 1);
+              const uint32_t two = odd ? pack2<BF16>(other, o[e + 1]) : pack2<BF16>(o[e], other);
+              if (has && e + (odd ? 1 : 0) < live) dst[(e + (odd ? 1 : 0)) * (DV / 2)] = two;
+            }
+          }
+        } else if (w4 == 0) {
+          if (lane < N) {
+            stat[lane] = m;
+            stat[N + lane] = sum_l;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(GB_ST + (pairs & 3)));
         }
       }
-      if constexpr (NC == 16) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
       __syncwarp();
-      wRow[lane] = l[0];
-      if (!vote(ok)) {
-        vote(false);
-        left_all = true;
-        break;
-      }
-      const int e0 = lane & (NC - 1);
-      const float sum_l = (gRow[e0] + gRow[32 + e0]) + (gRow[64 + e0] + gRow[96 + e0]);
-      float inv[NC];
-      spread(wMax, sum_l == 0.f ? 0.f : 1.f / sum_l, inv);
-      const float log_l = sum_l == 0.f ? SDPA_NEG_INF : m + __log2f(sum_l) + p.lse_shift;
-      if (w4 == 0 && lane < live) {
-        if (it.slot < 0)
-          p.lse[row0 + lane] = log_l * kLn2;
-        else
-          p.part_lse[it.slot * N + col0 + lane] = log_l;
-      }
-      ok = mbar_wait_w(bar(GB_O + (q & 1)), (q >> 1) & 1, ec, kSiteFwdSoftmax);
-      tc_fence_after();
-      float o[NC];
-      load(tO + N * (q & 1), o);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(GB_OE + (q & 1)));
-        mbar_arrive(bar(GB_IE + (u & 3)));
-      }
-      // (64 value columns: the product's rows lie on each warp's first 16 lanes)
-      const int d = DV == 128 ? own_key : w4 * 16 + lane;
-      const bool has = DV == 128 || lane < 16;
-#pragma unroll
-      for (int e = 0; e < NC; ++e) o[e] = inv[e] == 0.f ? 0.f : o[e] * inv[e];
-      if (it.slot >= 0) {
-        float* dst = p.part + static_cast<int64_t>(it.slot * N + col0) * DV + d;
-#pragma unroll
-        for (int e = 0; e < NC; ++e)
-          if (has && e < live) dst[e * DV] = o[e];
-      } else {
-        // two rows at a time: neighbouring lanes swap, and store two columns of a row each
-        const bool odd = (lane & 1) != 0;
-        uint32_t* dst = static_cast<uint32_t*>(p.o) + row0 * (DV / 2) + d / 2;
-#pragma unroll
-        for (int e = 0; e < NC; e += 2) {
-          const float other = __shfl_xor_sync(0xffffffffu, odd ? o[e] : o[e + 1], 1);
-          const uint32_t two = odd ? pack2<BF16>(other, o[e + 1]) : pack2<BF16>(o[e], other);
-          if (has && e + (odd ? 1 : 0) < live) dst[(e + (odd ? 1 : 0)) * (DV / 2)] = two;
-        }
-      }
+      if (lane == 0) mbar_arrive(bar(GB_IE + (u & 3)));
       ++q;
+      g0 += it.n;
+      if (both) ++pairs;
     }
     if (!left_all && !vote(ok)) vote(false);
   }
