@@ -23,6 +23,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   __shared__ float s_m[kJoinWarps * PER], s_l[kJoinWarps * PER];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x, x = blockIdx.y;
+  // (the next call's kernel may come: it waits for this one's end before it touches memory)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
   const int4 mine = __ldcg(p.runs + c);
   if (mine.x == 0 || mine.y == 0) return;

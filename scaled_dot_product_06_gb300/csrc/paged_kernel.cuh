@@ -82,7 +82,7 @@ struct PagedCfg {
 // unit full and read, statistics handed over, ring of units.
 enum : int { GB_KF = 0, GB_KE = GB_KF + 6, GB_VF = GB_KE + 6, GB_VE = GB_VF + 6, GB_Q = GB_VE + 6, GB_QE = GB_Q + 2,
              GB_S = GB_QE + 2, GB_P = GB_S + 2, GB_PV = GB_P + 2, GB_O = GB_PV + 2, GB_OE = GB_O + 2,
-             GB_ST = GB_OE + 2, GB_I = GB_ST + 4, GB_IE = GB_I + 4, GB_DRAIN = GB_IE + 4, GB_COUNT = GB_DRAIN + 2 };
+             GB_ST = GB_OE + 2, GB_I = GB_ST + 4, GB_IE = GB_I + 4, GB_DRAIN = GB_IE + 4, GB_START = GB_DRAIN + 2, GB_COUNT = GB_START + 2 };
 
 // One unit's part of a run, as the producer tells it.
 struct PagedItem {
@@ -165,40 +165,41 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-  // ---- this CTA's run: [lo, hi) of the line of all units
-  // thread i has the sequences [i per, (i + 1) per)
-  const int per = (p.B + C::THREADS - 1) / C::THREADS;
-  const int units = p.H_kv * p.row_blocks;  // of a sequence
-  const int length0 = tid * per < p.B ? __ldg(p.seqlen + tid * per) : 0;
-  if (tid == 0) {
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
-    
-#pragma unroll 1
-    for (int i = 0; i < GB_COUNT; ++i) {
+  if (warp == kSoftWarps) {
+    for (int i = lane; i < GB_COUNT; i += 32) {
       uint32_t n = 1;
       if ((i >= GB_P && i < GB_P + 2) || (i >= GB_OE && i < GB_OE + 2)) n = C::TURNS ? kSoftWarps / 2 : kSoftWarps;
       if (i >= GB_IE && i < GB_DRAIN) n = kSoftWarps + 2;
       mbar_init(bar(i), n);
     }
-    *abort_flag = 0u;
+    if (lane == 0) *abort_flag = 0u;
     fence_mbar_init();
-  }
-  if (warp == kSoftWarps + 1) {
+  } else if (warp == kSoftWarps + 1) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
+  } else if (warp == kSoftWarps + 2) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
   }
   // rows of Q that no box fills stay 0
 #pragma unroll 1
   for (int i = tid; i < C::Q_BUFS * C::Q_BYTES / 16; i += C::THREADS)
     reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
+  // (launched while the kernel before runs out: from here on its memory is looked at)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- this CTA's run: [lo, hi) of the line of all units
+  // thread i has the sequences [i per, (i + 1) per)
+  const int per = (p.B + C::THREADS - 1) / C::THREADS;
+  const int units = p.H_kv * p.row_blocks;  // of a sequence
   uint32_t sum = 0;
-  
 #pragma unroll 1
   for (int i = tid * per; i < min(p.B, (tid + 1) * per); ++i)
-    sum += static_cast<uint32_t>(paged_span(p, i == tid * per ? length0 : __ldg(p.seqlen + i)).n + kPagedCost);
+    sum += static_cast<uint32_t>(paged_span(p, __ldg(p.seqlen + i)).n + kPagedCost);
   sum *= static_cast<uint32_t>(units);
   uint32_t upto = sum;
 #pragma unroll
@@ -210,29 +211,27 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  uint32_t total = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kWarpsAll; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  const uint32_t run_lo = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
-  const uint32_t run_hi = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+  const uint32_t of_warp = lane < kWarpsAll ? scan[lane] : 0u;
+  const uint32_t total = __reduce_add_sync(0xffffffffu, of_warp);
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0u);
+  // equal runs, the first ones longer by one
+  const uint32_t each = total / gridDim.x, more = total - each * gridDim.x;
+  const uint32_t run_lo = each * blockIdx.x + min(blockIdx.x, more);
+  const uint32_t run_hi = run_lo + each + (blockIdx.x < more ? 1u : 0u);
   upto += before;
   if (run_lo < run_hi && run_lo >= upto - sum && run_lo < upto) {  // one thread of the CTA
     uint32_t at = run_lo - (upto - sum);
     int i = tid * per;
 #pragma unroll 1
     for (;; ++i) {
-      const int length = i == tid * per ? length0 : __ldg(p.seqlen + i);
-      const uint32_t w = static_cast<uint32_t>(paged_span(p, length).n + kPagedCost) * units;
+      const uint32_t w = static_cast<uint32_t>(paged_span(p, __ldg(p.seqlen + i)).n + kPagedCost) * units;
       if (at < w) break;
       at -= w;
     }
     start[0] = i;
     start[1] = static_cast<int>(at);
+    mbar_arrive(bar(GB_START));
   }
-  __syncthreads();
   const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const ErrCtx ec{p.err, abort_flag};
   auto next_item = [&](int u, PagedItem* it) -> bool {
@@ -271,8 +270,9 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
       return true;
     };
     // lengths of 32 sequences from l0 on, a lane each, and of the 32 after them
-    int l0 = start[0];
     uint32_t left = run_hi - run_lo;
+    if (left > 0 && !paged_wait(bar(GB_START), 0, ec, kSiteFwdLoad)) left = 0;
+    int l0 = start[0];
     auto length = [&](int i) { return i < p.B ? __ldg(p.seqlen + i) : 0; };
     int lens = left > 0 ? length(l0 + lane) : 0, lens_ahead = left > 0 ? length(l0 + 32 + lane) : 0;
     auto span_of = [&](int i) {  // i in [l0, l0 + 64)
@@ -403,6 +403,8 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
         sp_next = span_of(i + 1);
       }
     }
+    // (the kernel that joins the partials may come: it waits for this one's end by itself)
+    if (keys) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (ok) tell(PagedItem{-1, 0, 0, 0, 0, 0, 0});
     if (keys && lane == 0) p.runs[blockIdx.x] = runs;
     // Every copy issued must land before the CTA can retire; on the healthy path they
@@ -825,8 +827,17 @@ cudaError_t launch_paged_n(const CUtensorMap (&m)[3], const PagedParams& p, cuda
   auto kern = sdpa_paged_kernel<DQK, DV, BF16, N>;
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, 0);
   if (e != cudaSuccess) return e;
-  kern<<<p.grid, C::THREADS, C::SMEM, st>>>(m[0], m[1], m[2], p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], p);
 }
 
 template <int DQK, int DV, bool BF16>
