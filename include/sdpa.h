@@ -610,8 +610,8 @@ sdpa_status_t sdpa_fwd_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, i
  *   scale    as in sdpa_fwd; softcap 0 (none) or as in the capped calls.
  *   Heads    h_kv divides h; query head i reads K/V head i / (h / h_kv).
  *   Workspace  sdpa_fwd_paged_workspace_size(...) bytes, 256-byte aligned, whose
- *            contents do not matter. Two calls that may run at the same time need
- *            one each.
+ *            contents do not matter (none where a row of the table holds up to 512
+ *            keys). Two calls that may run at the same time need one each.
  * The work is cut by the lengths, on the device: neither table_width nor a mix
  * of lengths costs time. Results are the same bits in every run of the same
  * call; another batch around a sequence may cut its keys elsewhere and change
@@ -634,8 +634,8 @@ sdpa_status_t sdpa_qk_norm_rope_paged(int64_t b, int64_t s, int64_t h, int64_t h
                                       const void* k_weight, int weight_fp32, float eps,
                                       const int32_t* kv_slots, int64_t n_pages, int64_t page_size,
                                       void* stream);
-size_t sdpa_fwd_paged_workspace_size(int64_t h, int64_t h_kv, int64_t s_q, int64_t d_qk,
-                                     int64_t d_v);
+size_t sdpa_fwd_paged_workspace_size(int64_t h, int64_t h_kv, int64_t s_q, int64_t d_qk, int64_t d_v,
+                                     int64_t page_size, int64_t table_width);
 sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t d_qk,
                              int64_t d_v, float scale, float softcap, int64_t window_left,
                              sdpa_dtype_t dtype, const void* q, const sdpa_rows_t* k_pages,

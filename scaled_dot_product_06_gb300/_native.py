@@ -109,7 +109,7 @@ SIGNATURES = {
     "sdpa_qk_norm_rope_paged": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _int, _rows, _rows, _rows, _rows,
                                        _rows, _rows, _i64, _int, _ptr, _ptr, _i64, _ptr, _ptr, _ptr, _int, _f32,
                                        _ptr, _i64, _i64, _ptr]),
-    "sdpa_fwd_paged_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "sdpa_fwd_paged_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _i64]),
     "sdpa_fwd_paged": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _f32, _f32, _i64, _int, _ptr, _rows, _rows, _i64,
                               _i64, _ptr, _i64, _i64, _ptr, _ptr, _ptr, _ptr, _sz, _ptr]),
     "sdpa_bwd_noalloc": (_int, [_i64, _i64, _i64, _i64, _i64, _i64, _f32, _int, _f32, _u64, _u64,

@@ -11,10 +11,10 @@
 // that one entry needs of the others.
 //
 // Nothing here is worth more than a launch and three trips to memory (lengths,
-// then pages, then the stores): one cluster of CTAs, each of which scans all
+// then pages, then the stores): a few CTAs, each of which scans all
 // requests, 1024 at a time, and then takes its share of the tokens and table
-// entries, found by bisection of the sums in shared memory. A cluster, since
-// the lengths and the ring's counters may be advanced in place: they are
+// entries, found by bisection of the sums in shared memory. Where the lengths or
+// the ring's counters are advanced in place, the CTAs are a cluster, and they are
 // written after a barrier of all that read them.
 #include "common.cuh"
 #include "page_slots.cuh"
@@ -25,12 +25,21 @@ namespace {
 
 constexpr int kReq = 1024;  // threads, and requests scanned at a time
 constexpr int kWarps = kReq / 32;
-// Calls of more entries are shared by a cluster: a CTA takes 4096 in one go, and
-// the cluster's barrier costs about as much as another.
-constexpr int kCluster = 8;
-constexpr int64_t kAlone = 8192;
+// A CTA takes 4096 entries in one go; where there are more, more CTAs do, up to the
+// eight of a cluster where something is advanced in place. (Eight always took 19 us
+// of 131072 entries of 1000 requests.)
+constexpr int kCluster = 8, kCtas = 64;
+constexpr int64_t kShare = 4096;
 
 __device__ __forceinline__ uint32_t ceil_div(uint32_t a, uint32_t b) { return a / b + (a % b != 0 ? 1u : 0u); }
+
+// Page of a token; pages of a power of two (shift >= 0) without a division.
+__device__ __forceinline__ uint32_t page_of(uint32_t token, const PageSlotsParams& p) {
+  return p.shift >= 0 ? token >> p.shift : token / static_cast<uint32_t>(p.page);
+}
+__device__ __forceinline__ uint32_t pages_of(uint32_t tokens, const PageSlotsParams& p) {
+  return tokens > 0 ? page_of(tokens - 1, p) + 1u : 0u;
+}
 
 // Sums of tokens (held at `cap`, so that they stay in 32 bits; they matter only up
 // to the rows there are), pages asked for, pages given back.
@@ -51,11 +60,18 @@ struct Shared {
   uint8_t served[kReq];
   Sums warp[kWarps];
   Sums carry;
+  uint32_t taken;  // pages taken by served requests
 };
+
+// x modulo n, n > 0: counters below 2^32 without a 64-bit division.
+__device__ __forceinline__ uint32_t mod(uint64_t x, uint32_t n) {
+  return (x >> 32) == 0 ? static_cast<uint32_t>(x) % n : static_cast<uint32_t>(x % n);
+}
 
 // The first of n entries above x (n: none).
 __device__ __forceinline__ int above(const uint32_t* ends, int n, uint32_t x) {
   int lo = 0;
+#pragma unroll 1
   for (int step = kReq / 2; step > 0; step >>= 1)
     if (lo + step <= n && ends[lo + step - 1] <= x) lo += step;
   return lo < n && ends[lo] <= x ? lo + 1 : lo;
@@ -69,27 +85,28 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
   const bool packed = p.packed != 0;
   const uint32_t rows = static_cast<uint32_t>(p.rows), cap = packed ? rows + 1u : 0u;
   const int64_t head = p.range[0], tail = p.range[1];
+  int n_in = tid < p.b ? p.seqlens[tid] : 0, x_in = tid < p.b ? p.new_tokens[tid] : 0;  // of the chunk to come
+  if (tid == 0) s.taken = 0u;
+  __syncthreads();
   // (any contents of the counters stay inside the ring)
   const uint32_t avail =
       tail <= head ? 0u : static_cast<uint32_t>(min(static_cast<uint64_t>(tail) - static_cast<uint64_t>(head),
                                                     static_cast<uint64_t>(p.pool)));
-  const uint32_t head0 = p.pool > 0 ? static_cast<uint32_t>(static_cast<uint64_t>(head) % p.pool) : 0u;
-  const uint32_t tail0 = p.pool > 0 ? static_cast<uint32_t>(static_cast<uint64_t>(tail) % p.pool) : 0u;
+  const uint32_t head0 = p.pool > 0 ? mod(static_cast<uint64_t>(head), p.pool) : 0u;
+  const uint32_t tail0 = p.pool > 0 ? mod(static_cast<uint64_t>(tail), p.pool) : 0u;
   auto ring_at = [&](uint32_t from, uint32_t i) {  // i < pool
     const uint32_t at = from + i;
     return at >= p.pool ? at - p.pool : at;
   };
 
   Sums before{0u, 0u, 0u};  // of the requests before this chunk
-  uint32_t taken = 0;       // pages taken by served requests
   int len_out = 0;
   // Scans requests r0 .. r0 + kReq - 1 into s; returns this thread's new length.
   auto scan = [&](int r0) -> int {
-    const int r = r0 + tid;
-    const bool live = r < p.b;
-    const int n_in = live ? p.seqlens[r] : 0, x = live ? p.new_tokens[r] : 0;
+    const bool live = r0 + tid < p.b;
+    const int x = x_in;
     const uint32_t n = static_cast<uint32_t>(max(n_in, 0)), more = static_cast<uint32_t>(max(x, 0));
-    const uint32_t have = ceil_div(n, page), need = ceil_div(n + more, page);
+    const uint32_t have = pages_of(n, p), need = pages_of(n + more, p);
     const uint32_t wide = static_cast<uint32_t>(p.width);
     const bool room = live && x >= 0 && need <= wide;
     // (a padded request asks for pages when its tokens have entries; a packed one's
@@ -131,14 +148,17 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
     // served requests are the first ones in the order of their pages: the most taken is
     // the last one's sum
     const uint32_t upto = __reduce_max_sync(0xffffffffu, served && asked > 0 ? sum.take : 0u);
+    if (lane == 0 && upto > 0) atomicMax(&s.taken, upto);
     if (tid == kReq - 1) s.carry = sum;
+    // the next chunk's
+    const int next = r0 + kReq + tid;
+    n_in = next < p.b ? p.seqlens[next] : 0;
+    x_in = next < p.b ? p.new_tokens[next] : 0;
     __syncthreads();
-    if (lane == 0) s.warp[warp].tok = upto;
-    __syncthreads();
-    taken = max(taken, __reduce_max_sync(0xffffffffu, s.warp[lane].tok));
     return x < 0 ? 0 : static_cast<int>(served ? n + more : n);
   };
 
+#pragma unroll 1
   for (int r0 = 0; r0 < p.b; r0 += kReq) {
     len_out = scan(r0);
     const int n_req = min(kReq, p.b - r0);
@@ -150,69 +170,73 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
                                    : static_cast<uint32_t>(r0) * static_cast<uint32_t>(p.per);
     const uint32_t hi = packed ? min(after.tok, rows)
                                    : static_cast<uint32_t>(r0 + n_req) * static_cast<uint32_t>(p.per);
+#pragma unroll 1
     for (uint32_t g = lo / 4 + first; g < ceil_div(hi, 4); g += step) {
-      int slot[4], pos[4];
+      int4 slot = make_int4(-1, -1, -1, -1), pos = make_int4(0, 0, 0, 0);
       int i = 0;           // request of the chunk
       uint32_t end = 0;    // its last entry + 1 (0: none yet)
       uint32_t at = 0;     // page of the token before
       int id = -1;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t r = 4 * g + e;
-        slot[e] = -1;
-        pos[e] = 0;
-        if (r < lo || r >= hi) continue;
-        bool turn = false;  // another request's first token here
-        if (r >= end) {
-          if (packed) {
-            i = above(s.tok_end, n_req, r);
-            end = s.tok_end[i];
-          } else {
-            i = static_cast<int>(r / static_cast<uint32_t>(p.per)) - r0;
-            end = static_cast<uint32_t>(r0 + i + 1) * static_cast<uint32_t>(p.per);
+#pragma unroll 1
+      for (uint32_t r = 4 * g; r < 4 * g + 4; ++r) {
+        int own_slot = -1, own_pos = 0;
+        if (r >= lo && r < hi) {
+          const bool turn = r >= end;  // another request's first token here
+          if (turn) {
+            if (packed) {
+              i = above(s.tok_end, n_req, r);
+              end = s.tok_end[i];
+            } else {
+              i = static_cast<int>(r / static_cast<uint32_t>(p.per)) - r0;
+              end = static_cast<uint32_t>(r0 + i + 1) * static_cast<uint32_t>(p.per);
+            }
           }
-          turn = true;
+          const uint32_t start = packed ? (i > 0 ? s.tok_end[i - 1] : before.tok) : end - static_cast<uint32_t>(p.per);
+          const uint32_t t = r - start;
+          if (t < s.add[i]) {
+            const uint32_t place = s.len[i] + t, pg = page_of(place, p), off = place - pg * page;
+            own_pos = static_cast<int>(place);
+            if (s.served[i]) {
+              if (turn || id < 0 || pg != at) {
+                at = pg;
+                const uint32_t have = pages_of(s.len[i], p);
+                id = pg < have ? p.table[(r0 + i) * p.table_stride + pg]
+                               : fresh(s.take_end[i] - s.take[i] + pg - have);
+              }
+              if (id >= 0 && static_cast<uint32_t>(id) < p.pool) own_slot = static_cast<int>(id * page + off);
+            }
+          }
         }
-        // (packed: entries of a request are as many as its tokens; the one cut off by
-        // the last row has its sum held there, and its place from its first entry)
-        const uint32_t start = packed ? (i > 0 ? s.tok_end[i - 1] : before.tok)
-                                          : end - static_cast<uint32_t>(p.per);
-        const uint32_t t = r - start;
-        if (t >= s.add[i]) continue;
-        const uint32_t place = s.len[i] + t, pg = place / page, off = place - pg * page;
-        pos[e] = static_cast<int>(place);
-        if (!s.served[i]) continue;
-        if (turn || id < 0 || pg != at) {
-          at = pg;
-          const uint32_t have = ceil_div(s.len[i], page);
-          id = pg < have ? p.table[(r0 + i) * p.table_stride + pg]
-                         : fresh(s.take_end[i] - s.take[i] + pg - have);
-        }
-        if (id >= 0 && static_cast<uint32_t>(id) < p.pool) slot[e] = static_cast<int>(id * page + off);
+        slot = make_int4(slot.y, slot.z, slot.w, own_slot);
+        pos = make_int4(pos.y, pos.z, pos.w, own_pos);
       }
       if (4 * g >= lo && 4 * g + 4 <= hi) {
-        reinterpret_cast<int4*>(p.slots)[g] = make_int4(slot[0], slot[1], slot[2], slot[3]);
-        reinterpret_cast<int4*>(p.positions)[g] = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t r = 4 * g + e;
+        reinterpret_cast<int4*>(p.slots)[g] = slot;
+        reinterpret_cast<int4*>(p.positions)[g] = pos;
+      } else {  // shared with the chunk before or after, or the end
+#pragma unroll 1
+        for (uint32_t r = 4 * g; r < 4 * g + 4; ++r) {
           if (r >= lo && r < hi) {
-            p.slots[r] = slot[e];
-            p.positions[r] = pos[e];
+            p.slots[r] = slot.x;
+            p.positions[r] = pos.x;
           }
+          slot = make_int4(slot.y, slot.z, slot.w, 0);
+          pos = make_int4(pos.y, pos.z, pos.w, 0);
         }
       }
     }
     // ---- new entries of the table
-    for (uint32_t e = before.take + first; e < min(after.take, avail); e += step) {
+    // (by other warps than the tokens', where there are few of both)
+#pragma unroll 1
+    for (uint32_t e = before.take + (first ^ 512u); e < min(after.take, avail); e += step) {
       const int i = above(s.take_end, n_req, e);
       if (!s.served[i]) continue;
       const uint32_t j = e - (s.take_end[i] - s.take[i]);
-      p.table[(r0 + i) * p.table_stride + ceil_div(s.len[i], page) + j] = fresh(e);
+      p.table[(r0 + i) * p.table_stride + pages_of(s.len[i], p) + j] = fresh(e);
     }
     // ---- pages given back
-    for (uint32_t e = before.back + first; e < after.back; e += step) {
+#pragma unroll 1
+    for (uint32_t e = before.back + (first ^ 256u); e < after.back; e += step) {
       const int i = above(s.back_end, n_req, e);
       const uint32_t j = e - (i > 0 ? s.back_end[i - 1] : before.back);
       if (p.pool > 0) p.ring[ring_at(tail0, e % p.pool)] = p.table[(r0 + i) * p.table_stride + j];
@@ -226,13 +250,23 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
   }
   if (packed) {  // behind the last token
     if (p.b == 0 && first == 0) p.starts[0] = 0;
-    for (uint32_t r = before.tok + first; r < rows; r += step) {
-      p.slots[r] = -1;
-      p.positions[r] = 0;
+    const uint32_t lo = min(before.tok, rows);
+#pragma unroll 1
+    for (uint32_t g = lo / 4 + first; g < ceil_div(rows, 4); g += step) {
+      if (4 * g >= lo && 4 * g + 4 <= rows) {
+        reinterpret_cast<int4*>(p.slots)[g] = make_int4(-1, -1, -1, -1);
+        reinterpret_cast<int4*>(p.positions)[g] = make_int4(0, 0, 0, 0);
+      } else {
+#pragma unroll 1
+        for (uint32_t r = max(4 * g, lo); r < min(4 * g + 4, rows); ++r) {
+          p.slots[r] = -1;
+          p.positions[r] = 0;
+        }
+      }
     }
   }
   // ---- what may be advanced in place, after all have read it
-  if (ctas > 1) {
+  if (p.in_place && ctas > 1) {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   } else {
     __syncthreads();
@@ -243,6 +277,9 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
   } else {
     const Sums all = before;
     before = Sums{0u, 0u, 0u};
+    n_in = p.seqlens[tid];
+    x_in = p.new_tokens[tid];
+#pragma unroll 1
     for (int r0 = 0; r0 < p.b; r0 += kReq) {
       const int n = scan(r0);
       if (r0 + tid < p.b) p.seqlens_out[r0 + tid] = n;
@@ -252,7 +289,7 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
     before = all;
   }
   if (tid == 0) {
-    p.range_out[0] = head + taken;
+    p.range_out[0] = head + s.taken;
     p.range_out[1] = tail + before.back;
   }
 }
@@ -261,7 +298,9 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
 
 cudaError_t launch_page_slots(const PageSlotsParams& p, cudaStream_t st) {
   const int64_t entries = p.packed ? p.rows : static_cast<int64_t>(p.b) * p.per;
-  const unsigned ctas = entries > kAlone ? kCluster : 1;
+  const int64_t want = (entries + kShare - 1) / kShare, most = p.in_place ? kCluster : kCtas;
+  unsigned ctas = static_cast<unsigned>(want < 1 ? 1 : want > most ? most : want);
+  if (p.in_place && ctas > 1) ctas = kCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kReq);
@@ -271,7 +310,7 @@ cudaError_t launch_page_slots(const PageSlotsParams& p, cudaStream_t st) {
   at.val.clusterDim.x = ctas;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  cfg.numAttrs = p.in_place && ctas > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, page_slots_kernel, p);
 }
 

@@ -7,7 +7,8 @@ namespace sdpa {
 
 struct PageSlotsParams {
   int b;                   // requests
-  int page;                // tokens a page
+  int page, shift;         // tokens a page; its log2, or -1
+  int in_place;            // seqlens_out is seqlens or range_out is range
   int width;               // pages a row of the table holds
   int64_t table_stride;    // elements between its rows
   uint32_t pool;           // pages of the pool = entries of the ring

@@ -11,10 +11,14 @@ constexpr int kPagedTile = 128;   // keys a tile
 constexpr int kPagedBox = 64;     // most keys of one copy
 constexpr int kPagedCost = 1;     // what a unit costs besides its key tiles, in tiles
 constexpr int kPagedGrid = 152;   // CTAs at most: one an SM
+constexpr int kPagedWhole = 4;    // key tiles up to which units are not cut
 
 // A unit of work is a sequence, a K/V head and a block of its query rows. The
 // units of all sequences, each as long as its key tiles and kPagedCost, are one
-// line that is cut into as many equal runs as there are CTAs.
+// line that is cut into as many equal runs as there are CTAs. Where a sequence can have
+// no more than kPagedWhole key tiles (the host knows what a row of the table holds, not
+// the lengths), a unit has a length of 1 and is not cut: then there is nothing to
+// join, no second kernel and no workspace.
 struct PagedParams {
   int B, H_kv;
   int R, s_q;              // query rows of a K/V head: (h / h_kv) * s_q, row x of token x % s_q
@@ -32,6 +36,7 @@ struct PagedParams {
   int capped;
   uint32_t q_box;          // bytes of a 64-column box of Q
   int grid;
+  int whole;               // units are not cut
   // Partial rows of units cut by a run's end: run c leaves slot 2 c for the
   // unit it begins within and slot 2 c + 1 for the one it ends within.
   float* part;             // [2 grid][rows a block][d_v]

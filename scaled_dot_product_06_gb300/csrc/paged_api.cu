@@ -82,6 +82,9 @@ size_t paged_bytes(int64_t R, int64_t d_v) {
   return rows * (static_cast<size_t>(d_v) + 1) * sizeof(float) + kPagedGrid * sizeof(int4);
 }
 
+// Whether the units of sequences of up to `capacity` keys are left whole.
+bool whole_units(int64_t capacity) { return capacity <= kPagedWhole * kPagedTile; }
+
 // Heads and rows that both the size and the call check; *R: rows of a K/V head.
 sdpa_status_t check_rows_of(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t d_qk, int64_t d_v, int64_t* R) {
   if (b < 0 || h < 0 || s_q < 0) return fail(SDPA_ERR_INVALID_ARG, "sizes");
@@ -129,6 +132,8 @@ sdpa_status_t sdpa_page_slots(int64_t b, int64_t page_size, int64_t table_width,
   PageSlotsParams p{};
   p.b = static_cast<int>(b);
   p.page = static_cast<int>(page_size);
+  p.shift = (page_size & (page_size - 1)) == 0 ? log2_of(page_size) : -1;
+  p.in_place = seqlens_out == seqlens || free_range_out == free_range;
   p.width = static_cast<int>(table_width);
   p.table_stride = b > 1 ? table_stride : 0;
   p.pool = static_cast<uint32_t>(n_pages);
@@ -150,9 +155,12 @@ sdpa_status_t sdpa_page_slots(int64_t b, int64_t page_size, int64_t table_width,
   return SDPA_OK;
 }
 
-size_t sdpa_fwd_paged_workspace_size(int64_t h, int64_t h_kv, int64_t s_q, int64_t d_qk, int64_t d_v) {
+size_t sdpa_fwd_paged_workspace_size(int64_t h, int64_t h_kv, int64_t s_q, int64_t d_qk, int64_t d_v,
+                                     int64_t page_size, int64_t table_width) {
   int64_t R = 0;
   if (check_rows_of(1, h, h_kv, s_q, d_qk, d_v, &R) != SDPA_OK || R == 0) return 0;
+  if (page_size < 1 || table_width < 0 || page_size > kMaxKeys || table_width > kMaxKeys) return 0;
+  if (whole_units(page_size * table_width)) return 0;
   return (paged_bytes(R, d_v) + 255) & ~size_t(255);
 }
 
@@ -183,7 +191,8 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
   const int64_t capacity = n_pages > 0 ? table_width * page_size : 0;
   const int rows = paged_rows(static_cast<int>(R));
   const int64_t blocks = (R + rows - 1) / rows;
-  const int64_t line = b * h_kv * blocks * ((capacity + kPagedTile - 1) / kPagedTile + kPagedCost);
+  const bool whole = whole_units(table_width * page_size);
+  const int64_t line = b * h_kv * blocks * (whole ? 1 : (capacity + kPagedTile - 1) / kPagedTile + kPagedCost);
   if (blocks * h_kv > kMaxInt / b || line > kMaxInt) return fail(SDPA_ERR_UNSUPPORTED, "too many key tiles");
   if (!q || !o || !lse || !seqlen_k || (capacity > 0 && !block_table)) return fail(SDPA_ERR_INVALID_ARG, "null pointer");
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(seqlen_k, 4) || !aligned(block_table, 4))
@@ -192,8 +201,9 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
     if (sdpa_status_t s = check_pages(k_pages, n_pages, page_size, h_kv, "k_pages")) return s;
     if (sdpa_status_t s = check_pages(v_pages, n_pages, page_size, h_kv, "v_pages")) return s;
   }
-  if (workspace == nullptr || workspace_bytes < paged_bytes(R, d_v)) return fail(SDPA_ERR_WORKSPACE, "workspace");
-  if (!aligned(workspace, 256)) return fail(SDPA_ERR_MISALIGNED, "workspace");
+  if (!whole && (workspace == nullptr || workspace_bytes < paged_bytes(R, d_v)))
+    return fail(SDPA_ERR_WORKSPACE, "workspace");
+  if (!whole && !aligned(workspace, 256)) return fail(SDPA_ERR_MISALIGNED, "workspace");
 
   PagedParams p{};
   p.B = static_cast<int>(b);
@@ -227,9 +237,12 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
   const int box_q = static_cast<int>(std::min<int64_t>(R, rows));
   p.q_box = static_cast<uint32_t>(128 * box_q);
   p.grid = static_cast<int>(std::min<int64_t>(kPagedGrid, line));
-  p.part = static_cast<float*>(workspace);
-  p.part_lse = p.part + static_cast<int64_t>(2 * kPagedGrid) * rows * d_v;
-  p.runs = reinterpret_cast<int4*>(p.part_lse + static_cast<int64_t>(2 * kPagedGrid) * rows);
+  p.whole = whole ? 1 : 0;
+  if (!whole) {
+    p.part = static_cast<float*>(workspace);
+    p.part_lse = p.part + static_cast<int64_t>(2 * kPagedGrid) * rows * d_v;
+    p.runs = reinterpret_cast<int4*>(p.part_lse + static_cast<int64_t>(2 * kPagedGrid) * rows);
+  }
   p.o = o;
   p.lse = lse;
   CUtensorMap m[3];
@@ -252,7 +265,7 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
   const int di = static_cast<int>(d_qk), dvi = static_cast<int>(d_v);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = bf16 ? launch_paged_bf16(di, dvi, m, p, st) : launch_paged_fp16(di, dvi, m, p, st);
-  if (e == cudaSuccess) e = launch_paged_join(bf16, dvi, p, st);
+  if (e == cudaSuccess && !whole) e = launch_paged_join(bf16, dvi, p, st);
   if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, cudaGetErrorString(e));
   return SDPA_OK;
 }

@@ -137,6 +137,11 @@ __device__ __forceinline__ PagedSpan paged_span(const PagedParams& p, int seqlen
   return s;
 }
 
+// How long a unit of the sequence is on the line.
+__device__ __forceinline__ int paged_weight(const PagedParams& p, const PagedSpan& s) {
+  return p.whole ? 1 : s.n + kPagedCost;
+}
+
 template <int DQK, int DV, bool BF16, int N>
 __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
     sdpa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -151,11 +156,11 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + GB_COUNT);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  int* start = reinterpret_cast<int*>(tmem_slot + 2);              // sequence, place in it
-  uint32_t* scan = reinterpret_cast<uint32_t*>(tmem_slot + 4);     // [warps] sums
-  int* items = reinterpret_cast<int*>(tmem_slot + 4 + 16);         // ring of 4, 8 words each
+  int* start = reinterpret_cast<int*>(tmem_slot + 4);              // sequence, place in it, its length
+  uint32_t* scan = reinterpret_cast<uint32_t*>(tmem_slot + 8);     // [warps] sums
+  int* items = reinterpret_cast<int*>(tmem_slot + 8 + 16);         // ring of 4, 8 words each
   int* sIds = items + 32;                                          // [producers][32] pages
-  static_assert(GB_COUNT * 8 + 80 + 128 + 256 <= 1024 && GB_COUNT % 2 == 0, "barrier region");
+  static_assert(GB_COUNT * 8 + 96 + 128 + 256 <= 1024 && GB_COUNT % 2 == 0, "barrier region");
   // [softmax warps][NC] values of rows. While maxima are exchanged, sMax holds each
   // warp's and sRow is its own; at a unit's end sRow holds each warp's sums and sMax is
   // its own. Between the two uses lies a barrier of the warpgroup.
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
   uint32_t sum = 0;
 #pragma unroll 1
   for (int i = tid * per; i < min(p.B, (tid + 1) * per); ++i)
-    sum += static_cast<uint32_t>(paged_span(p, __ldg(p.seqlen + i)).n + kPagedCost);
+    sum += p.whole ? 1u : static_cast<uint32_t>(paged_weight(p, paged_span(p, __ldg(p.seqlen + i))));
   sum *= static_cast<uint32_t>(units);
   uint32_t upto = sum;
 #pragma unroll
@@ -224,8 +229,12 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
     int i = tid * per;
 #pragma unroll 1
     for (;; ++i) {
-      const uint32_t w = static_cast<uint32_t>(paged_span(p, __ldg(p.seqlen + i)).n + kPagedCost) * units;
-      if (at < w) break;
+      const int len = __ldg(p.seqlen + i);
+      const uint32_t w = static_cast<uint32_t>(paged_weight(p, paged_span(p, len))) * units;
+      if (at < w) {
+        start[2] = len;
+        break;
+      }
       at -= w;
     }
     start[0] = i;
@@ -269,41 +278,46 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
       ++nu;
       return true;
     };
-    // lengths of 32 sequences from l0 on, a lane each, and of the 32 after them
     uint32_t left = run_hi - run_lo;
     if (left > 0 && !paged_wait(bar(GB_START), 0, ec, kSiteFwdLoad)) left = 0;
-    int l0 = start[0];
-    auto length = [&](int i) { return i < p.B ? __ldg(p.seqlen + i) : 0; };
-    int lens = left > 0 ? length(l0 + lane) : 0, lens_ahead = left > 0 ? length(l0 + 32 + lane) : 0;
-    auto span_of = [&](int i) {  // i in [l0, l0 + 64)
-      const int near = __shfl_sync(0xffffffffu, lens, (i - l0) & 31), far = __shfl_sync(0xffffffffu, lens_ahead, (i - l0) & 31);
-      return paged_span(p, i - l0 < 32 ? near : far);
-    };
+    int i = 0, unit = 0, pos = 0;
+    PagedSpan sp{0, 0, 0}, sp_next{0, 0, 0};
     // A tile's copies are boxes of a page, of `box` keys each. Lane l has the page of
     // box ib + l of sequence is (in shared memory too, for the lane that copies), and of
     // the batch of boxes that is wanted next.
     const int per_tile = BN >> p.box_shift;
     int is = -1, ib = 0, ids = 0, as = -1, ab = 0, ids_ahead = 0;
     int* own_ids = sIds + (keys ? 0 : 32);
-    auto pages_of = [&](int i, int len, int b0) {
+    auto pages_of = [&](int i, int len, int b0) {  // (looked at, and held inside the pool, where it is used)
       const int key = (b0 + lane) << p.box_shift;
-      const int id = key < len ? __ldg(p.table + i * p.table_stride + (key >> p.page_shift)) : 0;
-      // (the first page behind the pool reads as zeros)
-      return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.n_pages) ? id : p.n_pages;
+      return key < len ? __ldg(p.table + i * p.table_stride + (key >> p.page_shift)) : 0;
     };
-    int i = l0, unit = 0, pos = 0;
-    PagedSpan sp{0, 0, 0}, sp_next{0, 0, 0};
+    int l0 = 0, lens = 0, lens_ahead = 0;
+    auto length = [&](int i) { return i < p.B ? __ldg(p.seqlen + i) : 0; };
+    auto first_tile = [&]() { return sp.lo + (p.whole ? 0 : max(pos - kPagedCost, 0)); };
     if (left > 0) {
-      sp = span_of(i);
-      sp_next = span_of(i + 1);
-      const int w = sp.n + kPagedCost;
+      i = l0 = start[0];
+      sp = paged_span(p, start[2]);
+      const int w = paged_weight(p, sp);
       unit = start[1] / w;
       pos = start[1] - unit * w;
+      // the first unit's pages at once, then the lengths of 32 sequences from l0 on, a
+      // lane each, and of the 32 after them
+      as = i;
+      ab = first_tile() * per_tile;
+      ids_ahead = pages_of(i, sp.len, ab);
+      lens = length(l0 + lane);
+      lens_ahead = length(l0 + 32 + lane);
     }
+    auto span_of = [&](int i) {  // i in [l0, l0 + 64)
+      const int near = __shfl_sync(0xffffffffu, lens, (i - l0) & 31), far = __shfl_sync(0xffffffffu, lens_ahead, (i - l0) & 31);
+      return paged_span(p, i - l0 < 32 ? near : far);
+    };
+    bool ahead_known = false;  // sp_next is that of sequence i + 1
     while (left > 0) {
-      const int w = sp.n + kPagedCost;
+      const int w = paged_weight(p, sp);
       const int take = static_cast<int>(min(left, static_cast<uint32_t>(w - pos)));
-      const int t0 = max(pos - kPagedCost, 0), t1 = max(pos + take - kPagedCost, 0);
+      const int t0 = p.whole ? 0 : max(pos - kPagedCost, 0), t1 = p.whole ? sp.n : max(pos + take - kPagedCost, 0);
       const bool none = sp.n == 0 && pos == 0;
       if (t1 > t0 || none) {
         PagedItem it;
@@ -343,27 +357,14 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
           const bool again = unit + 1 < units;  // the next unit is of the same sequence
           for (int j = 0; j < it.n; ++j) {
             const int box0 = (it.k0 + j) * per_tile;
-            if (j == 0 || box0 - ib == 32) {  // another batch of pages
-              const int want = box0;
-              if (is != i || ib != want) {
-                ids = as == i && ab == want ? ids_ahead : pages_of(i, sp.len, want);
-                is = i;
-                ib = want;
-                own_ids[lane] = ids;
-                __syncwarp();
-              }
-              // ... and the one after it: of this unit, of the next one of the
-              // sequence, or of the next sequence
-              if ((it.k0 + it.n) * per_tile > want + 32) {
-                as = i, ab = want + 32;
-                ids_ahead = pages_of(i, sp.len, ab);
-              } else if (again && sp.lo * per_tile != want) {
-                as = i, ab = sp.lo * per_tile;
-                ids_ahead = pages_of(i, sp.len, ab);
-              } else if (i + 1 < p.B && (as != i + 1 || ab != sp_next.lo * per_tile)) {
-                as = i + 1, ab = sp_next.lo * per_tile;
-                ids_ahead = pages_of(i + 1, sp_next.len, ab);
-              }
+            const bool batch = j == 0 || box0 - ib == 32;  // another batch of pages
+            if (batch && (is != i || ib != box0)) {
+              ids = as == i && ab == box0 ? ids_ahead : pages_of(i, sp.len, box0);
+              is = i;
+              ib = box0;
+              // (the first page behind the pool reads as zeros)
+              own_ids[lane] = static_cast<uint32_t>(ids) < static_cast<uint32_t>(p.n_pages) ? ids : p.n_pages;
+              __syncwarp();
             }
             if (!(ok = free_of(empty + s, round))) break;
             const int lo = max(box0, first), hi = min(box0 + per_tile, end);
@@ -385,6 +386,24 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
               s = 0;
               ++round;
             }
+            if (batch) {
+              // the batch after this one: of this unit, of the next one of the sequence,
+              // or of the next sequence
+              if (!ahead_known) {
+                sp_next = span_of(i + 1);
+                ahead_known = true;
+              }
+              if ((it.k0 + it.n) * per_tile > box0 + 32) {
+                as = i, ab = box0 + 32;
+                ids_ahead = pages_of(i, sp.len, ab);
+              } else if (again && sp.lo * per_tile != box0) {
+                as = i, ab = sp.lo * per_tile;
+                ids_ahead = pages_of(i, sp.len, ab);
+              } else if (i + 1 < p.B && (as != i + 1 || ab != sp_next.lo * per_tile)) {
+                as = i + 1, ab = sp_next.lo * per_tile;
+                ids_ahead = pages_of(i + 1, sp_next.len, ab);
+              }
+            }
           }
           if (!ok) break;
         }
@@ -399,14 +418,14 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
           lens = lens_ahead;
           lens_ahead = length(l0 + 32 + lane);
         }
-        sp = sp_next;
-        sp_next = span_of(i + 1);
+        sp = ahead_known ? sp_next : span_of(i);
+        ahead_known = false;
       }
     }
     // (the kernel that joins the partials may come: it waits for this one's end by itself)
     if (keys) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (ok) tell(PagedItem{-1, 0, 0, 0, 0, 0, 0});
-    if (keys && lane == 0) p.runs[blockIdx.x] = runs;
+    if (keys && lane == 0 && !p.whole) p.runs[blockIdx.x] = runs;
     // Every copy issued must land before the CTA can retire; on the healthy path they
     // did long ago.
     __syncwarp();

@@ -19,13 +19,13 @@ _pack_rows = struct.Struct("Pqqq").pack  # the bytes of an sdpa_rows_t
 
 def check_rows(name, t, shape, dtype, device):
     """The strides of a 4-D tensor with contiguous rows, of this type, shape and device."""
-    strides = t.stride()
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on the device of q")
+    strides = t.stride()
     if strides[3] != 1 and t.numel():
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     return strides
@@ -33,7 +33,7 @@ def check_rows(name, t, shape, dtype, device):
 
 def check_flat(name, t, shape, dtype, device):
     """The pointer of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on the device of q")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -53,7 +53,8 @@ def _head_rows(name, t, shape, dtype, device):
 
 
 def _check_output(name, t):
-    if 0 in t.stride() and any(st == 0 and n > 1 for n, st in zip(t.shape, t.stride())):
+    strides = t.stride()
+    if 0 in strides and any(st == 0 and n > 1 for n, st in zip(t.shape, strides)):
         raise ValueError(f"{name} must not be an expanded tensor")
 
 

@@ -201,12 +201,12 @@ def test_infinite_scores(scale):
 
 
 def test_writes_stay_inside():
-    x = make(3, 6, 2, 2, [2, 450, 77], 16, 128, 128, torch.bfloat16)
-    need = sdpa_fwd_paged_workspace_size(6, 2, 2, 128, 128)
+    x = make(3, 6, 2, 2, [2, 950, 77], 16, 128, 128, torch.bfloat16)
+    need = sdpa_fwd_paged_workspace_size(6, 2, 2, 128, 128, 16, 60)
     ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
     buf = torch.full((3 * 6 * 2 * 128 + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
     lb = torch.full((3 * 6 * 2 + 8,), 7.0, device="cuda")
-    wide = torch.full((3, 60), 1 << 30, dtype=torch.int32, device="cuda")
+    wide = torch.full((3, 80), 1 << 30, dtype=torch.int32, device="cuda")
     w = x["block_table"].shape[1]
     wide[:, 5:5 + w] = x["block_table"].cuda()
     g = cuda(x)
@@ -240,7 +240,7 @@ def test_pools_past_32_bits():
 
 def test_captured_graphs_that_share_a_workspace():
     """Two captured calls with one workspace, replayed in turn on lengths that change."""
-    need = sdpa_fwd_paged_workspace_size(16, 2, 1, 128, 128)
+    need = sdpa_fwd_paged_workspace_size(16, 2, 1, 128, 128, 16, 100)
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     xs = [make(b, 16, 2, 1, [n] * b, 16, 128, 128, torch.bfloat16, seed=b, garbage=False)
           for b, n in ((3, 2000), (1, 6000))]
@@ -309,7 +309,9 @@ def test_refusals():
         with pytest.raises(ValueError):
             sdpa_fwd_paged(**{**x, **bad})
     odd = torch.zeros(9, 2, 12, 64, dtype=torch.bfloat16, device="cuda")
-    for bad in (dict(k_pages=odd, v_pages=odd), dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
-                dict(k_pages=x["k_pages"][:1].expand(x["k_pages"].shape)), dict(softcap=-1.0), dict(scale=NAN)):
+    for bad in (dict(k_pages=odd, v_pages=odd), dict(k_pages=x["k_pages"][:1].expand(x["k_pages"].shape)), dict(softcap=-1.0), dict(scale=NAN)):
         with pytest.raises(RuntimeError):
             sdpa_fwd_paged(**{**x, **bad})
+    y = cuda(make(2, 4, 2, 1, [30, 600], 16, 64, 64, torch.bfloat16))
+    with pytest.raises(RuntimeError):
+        sdpa_fwd_paged(**y, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))

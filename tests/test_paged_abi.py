@@ -17,14 +17,14 @@ def rows_of(ptr=1 << 20, st=(2048, 64, 1024)):
 
 
 def fwd(lib, b=2, h=4, h_kv=2, s_q=1, d=64, d_v=64, scale=0.125, cap=0.0, left=-1, dtype=0, q=P, k=None, v=None,
-        n_pages=5, page=16, table=P, wide=7, stride=7, lens=P, o=P, lse=P, ws=P, nbytes=1 << 40):
+        n_pages=50, page=16, table=P, wide=70, stride=70, lens=P, o=P, lse=P, ws=P, nbytes=1 << 40):
     return lib.sdpa_fwd_paged(b, h, h_kv, s_q, d, d_v, scale, cap, left, dtype, q, k or rows_of(), v or rows_of(),
                               n_pages, page, table, wide, stride, lens, o, lse, ws, nbytes, None)
 
 
 def test_refusals(lib):  # noqa: F811
     for kw in (dict(b=-1), dict(s_q=-1), dict(h_kv=3), dict(h_kv=0), dict(n_pages=-1), dict(wide=-1),
-               dict(stride=6), dict(scale=float("nan")), dict(scale=float("inf")), dict(cap=-1.0), dict(cap=5000.0),
+               dict(stride=69), dict(scale=float("nan")), dict(scale=float("inf")), dict(cap=-1.0), dict(cap=5000.0),
                dict(cap=float("nan")), dict(scale=1e38, cap=1e-3), dict(q=NULL), dict(o=NULL), dict(lse=NULL),
                dict(table=NULL), dict(lens=NULL), dict(k=rows_of(ptr=None)), dict(v=rows_of(ptr=None)),
                dict(k=rows_of(st=(0, 64, 1024))), dict(v=rows_of(st=(2048, -64, 1024))),
@@ -41,6 +41,7 @@ def test_refusals(lib):  # noqa: F811
         assert fwd(lib, **kw) == ALIGN, kw
     assert fwd(lib, ws=NULL) == WS
     assert fwd(lib, nbytes=100) == WS
+    assert fwd(lib, wide=32, stride=32, ws=NULL, nbytes=0, q=NULL) == BAD  # (it needs none)
     for kw in (dict(b=0), dict(s_q=0), dict(h=0, h_kv=1)):
         assert fwd(lib, q=NULL, o=NULL, **kw) == OK, kw
 
@@ -49,9 +50,13 @@ def test_workspace_size(lib):  # noqa: F811
     size = lib.sdpa_fwd_paged_workspace_size
     for h, h_kv, s_q, rows in ((8, 8, 1, 16), (32, 2, 1, 16), (32, 2, 2, 32), (33, 1, 1, 64), (64, 1, 8, 64)):
         # two slots a CTA, rows of d_v + 1 floats, and 16 bytes a CTA
-        assert size(h, h_kv, s_q, 64, 64) == (304 * rows * 65 * 4 + 152 * 16 + 255) // 256 * 256
-        assert sdpa_fwd_paged_workspace_size(h, h_kv, s_q, 192, 128) == (304 * rows * 129 * 4 + 2432 + 255) // 256 * 256
-    assert size(8, 3, 1, 64, 64) == 0 and size(8, 2, 1, 96, 96) == 0 and size(8, 2, 0, 64, 64) == 0
+        assert size(h, h_kv, s_q, 64, 64, 16, 33) == (304 * rows * 65 * 4 + 152 * 16 + 255) // 256 * 256
+        assert sdpa_fwd_paged_workspace_size(h, h_kv, s_q, 192, 128, 1024, 7) == (304 * rows * 129 * 4 + 2432 + 255) // 256 * 256
+        # up to four key tiles a sequence: nothing to join
+        assert size(h, h_kv, s_q, 64, 64, 16, 32) == 0 and size(h, h_kv, s_q, 64, 64, 128, 0) == 0
+    for bad in ((8, 3, 1, 64, 64, 16, 99), (8, 2, 1, 96, 96, 16, 99), (8, 2, 0, 64, 64, 16, 99), (8, 2, 1, 64, 64, 0, 99),
+                (8, 2, 1, 64, 64, 16, -1), (8, 2, 1, 64, 64, 1 << 40, 1 << 40)):
+        assert size(*bad) == 0, bad
 
 
 def test_binding_refusals():
