@@ -32,7 +32,7 @@ struct PagedParams {
   const int* table;
   const int* seqlen;
   float scale_log2;        // factor of the raw score in the exponent
-  float cap_in, lse_shift; // capped scores: see cap_r8; lse_shift = softcap log2(e)
+  float cap_in;            // capped scores: factor of the raw score in the tanh (scale_log2 = softcap log2(e))
   int capped;
   uint32_t q_box;          // bytes of a 64-column box of Q
   int grid;
@@ -48,8 +48,8 @@ struct PagedParams {
   uint32_t* err;
 };
 
-// Rows a block: the columns of the score tiles, a multiple of 16.
-__host__ __device__ constexpr int paged_rows(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+// Rows a block.
+__host__ __device__ constexpr int paged_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
 cudaError_t launch_paged_bf16(int d_qk, int d_v, const CUtensorMap (&m)[3], const PagedParams& p, cudaStream_t st);
 cudaError_t launch_paged_fp16(int d_qk, int d_v, const CUtensorMap (&m)[3], const PagedParams& p, cudaStream_t st);

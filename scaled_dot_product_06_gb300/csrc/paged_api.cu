@@ -222,15 +222,13 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
   p.seqlen = seqlen_k;
   if (softcap != 0.f) {
     p.capped = 1;
-    p.cap_in = 2.f * kLog2e * scale / softcap;
-    p.scale_log2 = -2.f * kLog2e * softcap;
-    p.lse_shift = kLog2e * softcap;
+    p.cap_in = scale / softcap;
+    p.scale_log2 = kLog2e * softcap;
   } else if (scale == 0.f) {
     // every score 0: the capped form with a cap of 1 (the plain one masks raw
     // scores with infinities, which a zero factor would turn into NaN)
     p.capped = 1;
-    p.scale_log2 = -2.f * kLog2e;
-    p.lse_shift = kLog2e;
+    p.scale_log2 = kLog2e;
   } else {
     p.scale_log2 = scale * kLog2e;
   }

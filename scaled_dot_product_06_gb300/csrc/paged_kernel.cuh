@@ -9,13 +9,16 @@
 //
 // A decoding step reads each key once for a few rows, so the keys take the
 // products' long side: S^T = K Q^T has a tile of 128 keys on the tensor cores'
-// 128 lanes and N = 16, 32 or 64 rows as its columns, and O^T = V^T P^T the
+// 128 lanes and NR = 8, 16, 32 or 64 rows as its columns, and O^T = V^T P^T the
 // values' width on the lanes. A thread has one key: its rows' scores are its
 // registers, P^T goes back through shared memory (a key's rows side by side), and
 // only the maxima and sums cross threads: the sums once a unit, the maxima when
 // one has grown by more than 2^8, which a vote of the warpgroup finds out.
 // (With the rows on the lanes, as sdpa_prefix_kernel has them, a row of 8 keeps a
-// warp busy with 128 columns while the others idle.)
+// warp busy with 128 columns while the others idle.) The products read their long
+// operand from shared memory, and a few columns more cost them nothing: P goes in
+// as a high and a low part, each rounded to 16 bits, side by side, whose two O are
+// added at the end, so that its rounding (2^-9 in bf16, as much as O's own) is gone.
 //
 // The lengths are known on the device only. All units (sequence, K/V head, row
 // block) in a row, each as long as its key tiles, are one line, cut into equal
@@ -24,7 +27,7 @@
 // at most two slots a CTA, joined by a second kernel (paged_join.cu); the others
 // are written as they are.
 //
-// One persistent CTA an SM. Roles: two warpgroups of softmax threads (at N = 16 they
+// One persistent CTA an SM. Roles: two warpgroups of softmax threads (at NR = 8 and 16 they
 // take the key tiles in turns, each with a maximum, sum and O of its own, joined at
 // the unit's end by the one that had the last tile, while the other goes on; at 32
 // and 64 each has half of the rows), two producer warps, which both walk the run and
@@ -47,21 +50,23 @@
 
 namespace sdpa {
 
-template <int DQK, int DV, int N>
+template <int DQK, int DV, int NR>
 struct PagedCfg {
   static constexpr int BN = kPagedTile;
-  static constexpr bool TURNS = N == 16;               // the warpgroups take tiles in turns, else half of the rows each
-  static constexpr int NC = TURNS ? N : N / 2;         // rows a thread
+  static constexpr int N = NR < 16 ? 16 : NR;          // columns of S (an MMA of 128 lanes has 16 at least)
+  static constexpr int NP = 2 * NR;                    // columns of P and O: the high parts' rows, the low parts'
+  static constexpr bool TURNS = NR <= 16;              // the warpgroups take tiles in turns, else half of the rows each
+  static constexpr int NC = TURNS ? NR : NR / 2;       // rows a thread
   static constexpr int SOFT = 256;                     // softmax threads
   static constexpr int THREADS = SOFT + 128;
   static constexpr int K_BYTES = BN * DQK * 2;
   static constexpr int V_BYTES = BN * DV * 2;
   static constexpr int Q_BYTES = N * DQK * 2;
-  static constexpr int P_PITCH = N * 2;                // bytes a key of P^T: the swizzle's width
-  static constexpr int P_BYTES = BN * P_PITCH;
-  static constexpr int P_BUFS = N == 64 ? 1 : 2;
+  static constexpr int P_PITCH = NP < 64 ? NP * 2 : 128;  // bytes of a key in an atom of P^T: the swizzle's width
+  static constexpr int P_BYTES = BN * NP * 2;
+  static constexpr int P_BUFS = TURNS ? 2 : 1;
   // barriers and so on; two rows of NC floats a softmax warp; statistics handed over
-  static constexpr int MISC = 1024 + SOFT / 32 * NC * 8 + (TURNS ? 4 * N * 8 : 0);
+  static constexpr int MISC = 1024 + SOFT / 32 * NC * 8 + (TURNS ? 4 * NR * 8 : 0);
   static constexpr int Q_BUFS = Q_BYTES > 16384 ? 1 : 2;
   static constexpr int AVAIL = 227 * 1024 - 1024 - Q_BUFS * Q_BYTES - P_BUFS * P_BYTES - MISC;
   static constexpr int FIT = AVAIL / (K_BYTES + V_BYTES);
@@ -72,9 +77,10 @@ struct PagedCfg {
   static constexpr int OFF_P = OFF_Q + Q_BUFS * Q_BYTES;
   static constexpr int OFF_MISC = OFF_P + P_BUFS * P_BYTES;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
-  static constexpr uint32_t TMEM_COLS = TURNS ? 128 : 4 * N;
-  static constexpr uint32_t T_S = 0, T_O = 2 * N;      // S of two tiles; O of two units (of each warpgroup)
   static constexpr int OS = TURNS ? 2 : 1;
+  static constexpr uint32_t T_S = 0, T_O = 2 * N;      // S of two tiles; O of two units (of each warpgroup)
+  static constexpr uint32_t T_END = T_O + 2 * OS * NP;
+  static constexpr uint32_t TMEM_COLS = T_END <= 128 ? 128 : T_END <= 256 ? 256 : 512;
   static_assert(ST >= 2 && SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -93,11 +99,25 @@ struct PagedItem {
   int slot;       // partial slot, or -1: the whole unit
 };
 
+// P^T, a key's rows side by side (MN-major): atoms of 8 keys as wide as the swizzle.
 __device__ __forceinline__ uint64_t paged_desc_p(uint32_t saddr, int pitch) {
-  // rows of P^T side by side (MN-major), 8 keys an atom as wide as the swizzle
-  uint64_t d = sdesc_sw128(saddr, 16, 8 * pitch);
+  uint64_t d = sdesc_sw128(saddr, kPagedTile * 128, 8 * pitch);
   if (pitch < 128) d = (d & ~(uint64_t{7} << 61)) | (static_cast<uint64_t>(pitch == 64 ? 4 : 6) << 61);
   return d;
+}
+
+// tanh to about 2^-23 relative: z + z^3 q(z^2) up to 5/8, q a polynomial fitted to
+// it by reweighted least squares (2^-27.7), else 1 - 2 / (1 + e^(2 |z|)), which
+// loses nothing there. (cap_r8's form is good to 2^-20 of the cap, which a sum of
+// many rows, LSE, shows; here the keys' stream leaves time for this one.)
+__device__ __forceinline__ float paged_tanh(float z) {
+  const float a = fabsf(z), z2 = z * z;
+  const float far = copysignf(fmaf(-2.f, rcp(1.f + ex2(a * (2.f * kLog2e))), 1.f), z);
+  float q = fmaf(z2, -0.00570499f, 0.02063909f);
+  q = fmaf(z2, q, -0.05373972f);
+  q = fmaf(z2, q, 0.13331442f);
+  q = fmaf(z2, q, -0.3333328f);
+  return a < 0.625f ? fmaf(z * z2, q, z) : far;
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -142,12 +162,12 @@ __device__ __forceinline__ int paged_weight(const PagedParams& p, const PagedSpa
   return p.whole ? 1 : s.n + kPagedCost;
 }
 
-template <int DQK, int DV, bool BF16, int N>
-__global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
+template <int DQK, int DV, bool BF16, int NR>
+__global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     sdpa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p) {
-  using C = PagedCfg<DQK, DV, N>;
-  constexpr int ST = C::ST, NC = C::NC, BN = C::BN;
+  using C = PagedCfg<DQK, DV, NR>;
+  constexpr int ST = C::ST, N = C::N, NP = C::NP, NC = C::NC, BN = C::BN;
   constexpr int kWarpsAll = C::THREADS / 32, kSoftWarps = C::SOFT / 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -166,7 +186,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
   // its own. Between the two uses lies a barrier of the warpgroup.
   float* sMax = reinterpret_cast<float*>(smem + C::OFF_MISC + 1024);
   float* sRow = sMax + kSoftWarps * NC;
-  float* sStat = sRow + kSoftWarps * NC;  // [4][maximum, sum][N]: statistics of the other warpgroup's tiles
+  float* sStat = sRow + kSoftWarps * NC;  // [4][maximum, sum][NR]: statistics of the other warpgroup's tiles
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -346,7 +366,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
               mbar_arrive_expect_tx(bar(GB_Q + qb), (DQK / 64) * p.q_box);
 #pragma unroll
               for (int c = 0; c < DQK / 64; ++c)
-                tma_load_4d(sQ + qb * C::Q_BYTES + c * N * 128, &tmQ, bar(GB_Q + qb), c * 64, it.rb * N, it.b, it.hk);
+                tma_load_4d(sQ + qb * C::Q_BYTES + c * N * 128, &tmQ, bar(GB_Q + qb), c * 64, it.rb * NR, it.b, it.hk);
             }
             __syncwarp();
             ++nq;
@@ -482,7 +502,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
     mbar_wait(bar(GB_DRAIN), 0, ec, kSiteDrain, false);
   } else if (warp == kSoftWarps + 3) {
     // ------------------------------------------------- O^T = V^T P^T
-    constexpr uint32_t kIdO = idesc_f16(DV, N, BF16, true, true);
+    constexpr uint32_t kIdO = idesc_f16(DV, NP, BF16, true, true);
     const uint64_t dV0 = sdesc_sw128(sV, BN * 128, 1024), dP0 = paged_desc_p(sP, C::P_PITCH);
     int g = 0, q = 0, s = 0;
     uint32_t ph = 0;
@@ -522,7 +542,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
         tc_fence_after();
         const uint64_t dV = desc_adv(dV0, s * C::V_BYTES);
         const uint64_t dP = desc_adv(dP0, (C::P_BUFS == 2 ? (g & 1) : 0) * C::P_BYTES);
-        const uint32_t dO = tbase + C::T_O + N * (C::TURNS ? 2 * ob + (g & 1) : ob);
+        const uint32_t dO = tbase + C::T_O + NP * (C::TURNS ? 2 * ob + (g & 1) : ob);
         const bool first = j < C::OS;  // of the tiles that this O sums
         if (elect_one_sync()) {
           if (k1 - k0 == BN / 16) {
@@ -558,7 +578,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
     const uint32_t tS = tbase + C::T_S + col0 + own_lanes;
     // O of the item's tiles (turns: those of warpgroup w)
     auto tO = [&](int q, int w) {
-      return tbase + C::T_O + N * (C::TURNS ? 2 * (q & 1) + w : (q & 1)) + col0 + own_lanes;
+      return tbase + C::T_O + NP * (C::TURNS ? 2 * (q & 1) + w : (q & 1)) + col0 + own_lanes;
     };
     float* gMax = sMax + t * 4 * NC;
     float* gRow = sRow + t * 4 * NC;
@@ -567,20 +587,28 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
     const int own_row = lane & (NC - 1);
     const float sl2 = p.scale_log2;
     const float hide = sl2 < 0.f ? -SDPA_NEG_INF : SDPA_NEG_INF;  // masked raw score
-    // 16-byte chunk of a key's row of P^T, as the swizzle has it
+    // 16-byte chunk of a key's row of P^T (0 .. NP / 8 - 1), as the swizzle has it
     const int flip = C::P_PITCH == 128 ? own_key & 7 : C::P_PITCH == 64 ? (own_key >> 1) & 3 : (own_key >> 2) & 1;
     uint8_t* own_p = smem + C::OFF_P + own_key * C::P_PITCH;
+    auto chunk_at = [&](int c) {
+      return C::P_PITCH == 128 ? (c >> 3) * BN * 128 + (((c & 7) ^ flip) << 4) : (c ^ flip) << 4;
+    };
     // A vote of the warpgroup. A warp whose wait ran out votes no until all leave
     // together: after a no comes a second vote, on whether all are well.
     auto vote = [&](bool yes) { return named_bar_and(1 + t, 128, yes); };
     auto load = [&](uint32_t at, float (&x)[NC]) {
       if constexpr (NC == 32) {
         tmem_ld32f(at, x);
-      } else {
+      } else if constexpr (NC == 16) {
         uint32_t r[16];
         tmem_ld16(at, r);
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]);
+      } else {
+        uint32_t r[8];
+        tmem_ld8(at, r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(r[e]);
       }
     };
     auto spread = [&](float* own, float v, float (&x)[NC]) {  // lane e's value of row e to all lanes
@@ -605,7 +633,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
     bool ok = true, left_all = false;
     PagedItem it;
     for (; (ok = next_item(u, &it)) && it.n >= 0; ++u) {
-      const int base = it.rb * N + col0;  // of the K/V head's rows
+      const int base = it.rb * NR + col0;  // of the K/V head's rows
       const int live = min(NC, p.R - base);
       const int64_t row0 = (static_cast<int64_t>(it.b) * p.H_kv + it.hk) * p.R + base;
       if (it.n == 0) {  // a sequence without a key
@@ -637,7 +665,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
         tmem_wait_ld();
         if (p.capped) {
 #pragma unroll
-          for (int e = 0; e < NC; ++e) x[e] = rcp(1.f + ex2(x[e] * p.cap_in));
+          for (int e = 0; e < NC; ++e) x[e] = paged_tanh(x[e] * p.cap_in);
         }
         const bool hidden = key0 + BN - 1 > last0 || (p.left >= 0 && key0 < last0 + p.s_q - 1 - p.left);
         bool out = false;  // a key that no row sees
@@ -693,16 +721,19 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
             const int before = g - C::OS;
             if (ok) ok = paged_wait(bar(GB_PV + (before & 1)), (before >> 1) & 1, ec, kSiteFwdSoftmax);
             tc_fence_after();
-            load(tO(q, t), o);
-            tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < NC; ++e) l[e] *= al[e];
 #pragma unroll
-            for (int e0 = 0; e0 < NC; e0 += 16) {
-              uint32_t r[16];
+            for (int h = 0; h < 2; ++h) {  // the high parts' O, the low parts'
+              load(tO(q, t) + h * NR, o);
+              tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e0 + e] * al[e0 + e]);
-              tmem_st16(tO(q, t) + e0, r);
+              for (int e0 = 0; e0 < NC; e0 += 8) {
+                uint32_t r[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(o[e0 + e] * al[e0 + e]);
+                tmem_st8(tO(q, t) + h * NR + e0, r);
+              }
             }
             tmem_wait_st();
           }
@@ -721,10 +752,17 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
         }
         uint8_t* to = own_p + (C::P_BUFS == 2 ? (g & 1) : 0) * C::P_BYTES;
 #pragma unroll
-        for (int e = 0; e < NC; e += 8)
-          *reinterpret_cast<uint4*>(to + (((col0 + e) / 8) ^ flip) * 16) =
-              make_uint4(pack2<BF16>(x[e], x[e + 1]), pack2<BF16>(x[e + 2], x[e + 3]),
-                         pack2<BF16>(x[e + 4], x[e + 5]), pack2<BF16>(x[e + 6], x[e + 7]));
+        for (int e = 0; e < NC; e += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            hi[i] = pack2<BF16>(x[e + 2 * i], x[e + 2 * i + 1]);
+            const float2 f = unpack2<BF16>(hi[i]);
+            lo[i] = pack2<BF16>(x[e + 2 * i] - f.x, x[e + 2 * i + 1] - f.y);
+          }
+          *reinterpret_cast<uint4*>(to + chunk_at((col0 + e) / 8)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to + chunk_at((NR + col0 + e) / 8)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -744,7 +782,8 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
             l[e] = keep + __shfl_xor_sync(0xffffffffu, send, o);
           }
         }
-        if constexpr (NC == 16) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+#pragma unroll
+        for (int o = NC; o < 32; o *= 2) l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
         __syncwarp();
         if (lane < NC) wRow[lane] = l[0];
         if (!vote(ok)) {
@@ -753,13 +792,13 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
           break;
         }
         float sum_l = (gRow[own_row] + gRow[NC + own_row]) + (gRow[2 * NC + own_row] + gRow[3 * NC + own_row]);
-        float* stat = sStat + (pairs & 3) * 2 * N;
+        float* stat = sStat + (pairs & 3) * 2 * NR;
         if (ends) {
           // ---- the unit's rows: O / l, and the log of the sum of exponentials
           float c_own = 1.f, c_other = 0.f;
           if (both) {  // join the other warpgroup's tiles
             ok = paged_wait(bar(GB_ST + (pairs & 3)), (pairs >> 2) & 1, ec, kSiteFwdSoftmax);
-            const float m2 = stat[own_row], l2 = stat[N + own_row], top = fmaxf(m, m2);
+            const float m2 = stat[own_row], l2 = stat[NR + own_row], top = fmaxf(m, m2);
             const float b = top == SDPA_NEG_INF ? 0.f : top;
             c_own = ex2(m - b);
             c_other = ex2(m2 - b);
@@ -770,28 +809,28 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
           float c[NC], c2[NC], o[NC];
           spread(wMax, c_own * inv, c);
           if (both) spread(wMax, c_other * inv, c2);
-          const float log_l = sum_l == 0.f ? SDPA_NEG_INF : m + __log2f(sum_l) + p.lse_shift;
+          const float log_l = sum_l == 0.f ? SDPA_NEG_INF : m + __log2f(sum_l);
           if (w4 == 0 && lane < live) {
             if (it.slot < 0)
               p.lse[row0 + lane] = log_l * kLn2;
             else
-              p.part_lse[it.slot * N + col0 + lane] = log_l;
+              p.part_lse[it.slot * NR + col0 + lane] = log_l;
           }
           ok = paged_wait(bar(GB_O + (q & 1)), (q >> 1) & 1, ec, kSiteFwdSoftmax) && ok;
           tc_fence_after();
-          load(tO(q, t), o);
-          if (both) {
-            float o2[NC];
-            load(tO(q, t ^ 1), o2);
+          auto take = [&](int w, const float (&f)[NC], bool add) {  // o (+)= f times warpgroup w's O
+            float hi[NC], lo[NC];
+            load(tO(q, w), hi);
+            load(tO(q, w) + NR, lo);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < NC; ++e)
-              o[e] = (c[e] == 0.f ? 0.f : o[e] * c[e]) + (c2[e] == 0.f ? 0.f : o2[e] * c2[e]);
-          } else {
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < NC; ++e) o[e] = c[e] == 0.f ? 0.f : o[e] * c[e];
-          }
+            for (int e = 0; e < NC; ++e) {
+              const float v = f[e] == 0.f ? 0.f : (hi[e] + lo[e]) * f[e];
+              o[e] = add ? o[e] + v : v;
+            }
+          };
+          take(t, c, false);
+          if (both) take(t ^ 1, c2, true);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(GB_OE + (q & 1)));
@@ -799,7 +838,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
           const int d = DV == 128 ? own_key : w4 * 16 + lane;
           const bool has = DV == 128 || lane < 16;
           if (it.slot >= 0) {
-            float* dst = p.part + static_cast<int64_t>(it.slot * N + col0) * DV + d;
+            float* dst = p.part + static_cast<int64_t>(it.slot * NR + col0) * DV + d;
 #pragma unroll
             for (int e = 0; e < NC; ++e)
               if (has && e < live) dst[e * DV] = o[e];
@@ -815,9 +854,9 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
             }
           }
         } else if (w4 == 0) {
-          if (lane < N) {
+          if (lane < NR) {
             stat[lane] = m;
-            stat[N + lane] = sum_l;
+            stat[NR + lane] = sum_l;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(GB_ST + (pairs & 3)));
@@ -840,10 +879,10 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, N>::THREADS, 1)
   }
 }
 
-template <int DQK, int DV, bool BF16, int N>
+template <int DQK, int DV, bool BF16, int NR>
 cudaError_t launch_paged_n(const CUtensorMap (&m)[3], const PagedParams& p, cudaStream_t st) {
-  using C = PagedCfg<DQK, DV, N>;
-  auto kern = sdpa_paged_kernel<DQK, DV, BF16, N>;
+  using C = PagedCfg<DQK, DV, NR>;
+  auto kern = sdpa_paged_kernel<DQK, DV, BF16, NR>;
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, 0);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -862,6 +901,7 @@ cudaError_t launch_paged_n(const CUtensorMap (&m)[3], const PagedParams& p, cuda
 template <int DQK, int DV, bool BF16>
 cudaError_t launch_paged_d(const CUtensorMap (&m)[3], const PagedParams& p, cudaStream_t st) {
   switch (paged_rows(p.R)) {
+    case 8: return launch_paged_n<DQK, DV, BF16, 8>(m, p, st);
     case 16: return launch_paged_n<DQK, DV, BF16, 16>(m, p, st);
     case 32: return launch_paged_n<DQK, DV, BF16, 32>(m, p, st);
     default: return launch_paged_n<DQK, DV, BF16, 64>(m, p, st);
