@@ -125,6 +125,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_binding = None
 
 
 class SdpaError(RuntimeError):
@@ -148,6 +149,25 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = handle
     return _lib
+
+
+def binding():
+    """The native binding's module (csrc/binding.cpp, linked to the same library)."""
+    global _binding
+    if _binding is None:
+        lib()
+        path = os.path.join(os.path.dirname(LIB_PATH), "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (the libraries that it is linked to)
+        spec = importlib.util.spec_from_file_location(
+            "_binding", path, loader=importlib.machinery.ExtensionFileLoader("_binding", path))
+        _binding = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_binding)
+    return _binding
 
 
 def status_string(status: int) -> str:

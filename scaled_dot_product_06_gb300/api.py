@@ -50,6 +50,31 @@ def _run(t: torch.Tensor, name: str, *args) -> None:
         _native.check(st, name)
 
 
+def call_native(name: str, stream, t: torch.Tensor, given, *args):
+    """The native binding's call of the entry point sdpa_<name>, on ``stream`` (None: the
+    current one) for tensors on t's device. given: the outputs that were passed, in the
+    order of the returned ones (see new_tensor for the others)."""
+    fn = getattr(_native.binding(), name)
+    if stream is None:
+        out = fn(*args)
+    else:
+        if not t.is_cuda:
+            raise ValueError("a stream for tensors that are not on a CUDA device")
+        _stream_ptr(stream, t)  # (its device)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=t.device)
+        caller = torch.cuda.current_stream(t.device)
+        with torch.cuda.stream(stream):
+            out = fn(*args)
+        if stream != caller and not isinstance(out, int):
+            for o, g in zip(out, given):
+                if g is None and o is not None:
+                    o.record_stream(caller)
+    if isinstance(out, int):
+        _native.check(out, "sdpa_" + name)
+    return out
+
+
 def new_tensor(shape, dtype, device, stream, scratch=False) -> torch.Tensor:
     """Memory for a call on ``stream`` (None: the current one).
 

@@ -4,6 +4,8 @@ Each CUDA translation unit under ``csrc/`` is compiled in parallel into
 ``_build/`` and linked into ``libsdpa.so`` next to this file. The CUDA runtime
 is linked statically; the driver entry point for TMA descriptor encoding is
 looked up at run time, so the library loads on machines without a GPU.
+``_binding.so``, the native binding of the calls with the shortest kernels, is
+compiled by g++ against torch's headers and linked to that library.
 """
 from __future__ import annotations
 
@@ -12,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsdpa.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.cu", "aux.cu", "noalloc.cu", "fwd_bf16.cu", "fwd_fp16.cu", "bwd_dkdv_bf16.cu",
            "bwd_dkdv_fp16.cu", "bwd_dq_bf16.cu", "bwd_dq_fp16.cu", "bwd_fused_bf16.cu",
            "bwd_fused_fp16.cu", "fwd_cap.cu", "bwd_dkdv_cap_bf16.cu", "bwd_dkdv_cap_fp16.cu",
@@ -48,18 +52,45 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _run(cmd: list[str], what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding() -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c", os.path.join(CSRC, "binding.cpp"),
+          "-o", obj], "g++ on binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, LIB, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "link of _binding.so")
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     """Compile every translation unit and link libsdpa.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
-    jobs = jobs or min(len(SOURCES), os.cpu_count() or 1)
+    jobs = jobs or min(len(SOURCES) + 1, os.cpu_count() or 1)
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run(cmd, "link of libsdpa.so")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

@@ -12,7 +12,7 @@ import struct
 import torch
 
 from . import _native
-from .api import _DTYPE_CODE, _ptr, _run, _stream_ptr, check_workspace, new_tensor
+from .api import _DTYPE_CODE, _ptr, _run, _stream_ptr, call_native, check_workspace, new_tensor
 
 _pack_rows = struct.Struct("Pqqq").pack  # the bytes of an sdpa_rows_t
 
@@ -116,62 +116,8 @@ def sdpa_qk_norm_rope(q, k, cos, sin, *, v=None, positions=None, q_weight=None, 
     a paged cache instead: each token goes to row slot % page_size of page
     slot // page_size, or nowhere where the slot is outside the pages (see
     sdpa_page_slots)."""
-    _check_qkv(q, k, v)
-    b, s, h, d = q.shape
-    h_kv, dt, dev = k.shape[2], q.dtype, q.device
-    d_v = d if v is None else v.shape[3]
-    q_in = _token_rows("q", q, (b, s, h, d), dt, dev)
-    k_in = _token_rows("k", k, (b, s, h_kv, d), dt, dev)
-    v_in = None if v is None else _token_rows("v", v, (b, s, h_kv, d_v), dt, dev)
-    if v is None and v_out is not None:
-        raise ValueError("v_out without v")
-    rot, cos_p, sin_p, n_pos, pos_p = _table(dev, cos, sin, positions, b, s)
-    qw_p, kw_p, fp32 = _weights(dt, dev, q_weight, k_weight, d)
-    outer, cache, rows_p = b, s, None
-    if kv_slots is not None:
-        if kv_rows is not None:
-            raise ValueError("either kv_rows or kv_slots")
-        rows_p = check_flat("kv_slots", kv_slots, (b, s), torch.int32, dev)
-        if k_out is None or (v is not None and v_out is None):
-            raise ValueError("kv_slots needs the pages as k_out (and v_out)")
-        if k_out.dim() != 4:
-            raise ValueError("k_out must have 4 dimensions")
-        outer, _, cache, _ = k_out.shape
-    elif kv_rows is not None:
-        rows_p = check_flat("kv_rows", kv_rows, (b,), torch.int32, dev)
-        if k_out is None or (v is not None and v_out is None):
-            raise ValueError("kv_rows needs the caches as k_out (and v_out)")
-        cache = k_out.shape[2] if k_out.dim() == 4 else -1
-    # outputs: new ones are contiguous
-    row, kv_shape = d, (outer, h_kv, cache, d)
-    if q_out is None:
-        q_out = new_tensor((b, h, s, d), dt, dev, stream)
-        q_to = _pack_rows(q_out.data_ptr(), h * s * row, row, s * row)
-    else:
-        q_to = _head_rows("q_out", q_out, (b, h, s, d), dt, dev)
-        _check_output("q_out", q_out)
-    if k_out is None:
-        k_out = new_tensor(kv_shape, dt, dev, stream)
-        k_to = _pack_rows(k_out.data_ptr(), h_kv * s * row, row, s * row)
-    else:
-        k_to = _head_rows("k_out", k_out, kv_shape, dt, dev)
-        _check_output("k_out", k_out)
-    v_to = None
-    if v is not None:
-        if v_out is None:
-            v_out = new_tensor((b, h_kv, s, d_v), dt, dev, stream)
-        else:
-            _check_output("v_out", v_out)
-        v_to = _head_rows("v_out", v_out, (outer, h_kv, cache, d_v), dt, dev)
-    if kv_slots is not None:
-        _run(q, "sdpa_qk_norm_rope_paged", b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], q_in, k_in, v_in, q_to, k_to,
-             v_to, rot, int(bool(interleaved)), cos_p, sin_p, n_pos, pos_p, qw_p, kw_p, fp32, eps, rows_p, outer,
-             cache, _stream_ptr(stream, q))
-        return q_out, k_out, v_out
-    _run(q, "sdpa_qk_norm_rope", b, s, h, h_kv, d, d_v, _DTYPE_CODE[dt], q_in, k_in, v_in, q_to, k_to, v_to,
-         rot, int(bool(interleaved)), cos_p, sin_p, n_pos, pos_p, qw_p, kw_p, fp32, eps, rows_p, cache,
-         _stream_ptr(stream, q))
-    return q_out, k_out, v_out
+    return call_native("qk_norm_rope", stream, q, (q_out, k_out, v_out), q, k, cos, sin, v, positions, q_weight,
+                       k_weight, eps, interleaved, kv_rows, kv_slots, q_out, k_out, v_out)
 
 
 @functools.lru_cache(maxsize=256)
