@@ -73,8 +73,9 @@ def _compile_binding() -> str:
 def _link_binding(obj: str) -> None:
     import torch
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, LIB, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
-          "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "link of _binding.so")
+    _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L" + HERE, "-l:libsdpa.so",
+          "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda",
+          "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "link of _binding.so")
     os.replace(BINDING + ".tmp", BINDING)
 
 

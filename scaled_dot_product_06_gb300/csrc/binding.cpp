@@ -9,8 +9,10 @@
 
 #include <cmath>
 #include <cstdarg>
+#include <optional>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -79,9 +81,14 @@ T* flat(const char* name, const Tensor& t, ScalarType type, const Place& at, Int
   return static_cast<T*>(t.data_ptr());
 }
 
+// Memory of the current stream (past the dispatcher: it takes as long as the rest).
+Tensor fresh(IntArrayRef shape, ScalarType type, const Tensor& like) {
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+}
+
 // A new tensor, or the given one, checked.
 Tensor made(const char* name, PyObject* given, ScalarType type, const Tensor& like, const Place& at, IntArrayRef shape) {
-  if (given == Py_None) return at::empty(shape, like.options().dtype(type));
+  if (given == Py_None) return fresh(shape, type, like);
   const Tensor& t = tensor(given, name);
   flat(name, t, type, at, shape);
   return t;
@@ -229,7 +236,7 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     bytes = w->nbytes();
   } else {
     bytes = sdpa_fwd_paged_workspace_size(h, h_kv, s_q, d_qk, d_v, page, table.width);
-    if (bytes > 0) scratch = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
+    if (bytes > 0) scratch = fresh({static_cast<int64_t>(bytes)}, at::kByte, q);
   }
   const sdpa_status_t st = call(at, [&](void* stream) {
     return sdpa_fwd_paged(b, h, h_kv, s_q, d_qk, d_v, static_cast<float>(scale), static_cast<float>(softcap), left, type,
@@ -303,7 +310,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor out[3];
   auto target = [&](const char* name, const Tensor* given, IntArrayRef shape, Tensor* t) {
     if (given == nullptr) {
-      *t = at::empty(shape, q.options());
+      *t = fresh(shape, dt, q);
     } else {
       *t = *given;
     }

@@ -163,8 +163,6 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
     len_out = scan(r0);
     const int n_req = min(kReq, p.b - r0);
     const Sums after = s.carry;
-    // the page ids of new pages, from the ring
-    auto fresh = [&](uint32_t i) { return p.ring[ring_at(head0, i)]; };
     // ---- tokens, four at a time
     const uint32_t lo = packed ? min(before.tok, rows)
                                    : static_cast<uint32_t>(r0) * static_cast<uint32_t>(p.per);
@@ -172,44 +170,58 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
                                    : static_cast<uint32_t>(r0 + n_req) * static_cast<uint32_t>(p.per);
 #pragma unroll 1
     for (uint32_t g = lo / 4 + first; g < ceil_div(hi, 4); g += step) {
-      int4 slot = make_int4(-1, -1, -1, -1), pos = make_int4(0, 0, 0, 0);
-      int i = 0;           // request of the chunk
-      uint32_t end = 0;    // its last entry + 1 (0: none yet)
-      uint32_t at = 0;     // page of the token before
-      int id = -1;
+      // where the tokens' page numbers are, and their rows of the page; the four are
+      // then fetched together
+      const int* where[4] = {nullptr, nullptr, nullptr, nullptr};
+      uint32_t off[4] = {0u, 0u, 0u, 0u};
+      int4 pos = make_int4(0, 0, 0, 0);
+      int i = -1;                       // request of the chunk
+      uint32_t start = 0, end = 0;      // its entries
 #pragma unroll 1
       for (uint32_t r = 4 * g; r < 4 * g + 4; ++r) {
-        int own_slot = -1, own_pos = 0;
+        const int* own = nullptr;
+        uint32_t own_off = 0;
+        int own_pos = 0;
         if (r >= lo && r < hi) {
-          const bool turn = r >= end;  // another request's first token here
-          if (turn) {
+          if (r >= end) {  // another request's first token here
             if (packed) {
-              i = above(s.tok_end, n_req, r);
+              if (i < 0) {
+                i = above(s.tok_end, n_req, r);
+              } else {  // the next one that has tokens
+#pragma unroll 1
+                while (s.tok_end[i] <= r) ++i;
+              }
+              start = i > 0 ? s.tok_end[i - 1] : before.tok;
               end = s.tok_end[i];
             } else {
-              i = static_cast<int>(r / static_cast<uint32_t>(p.per)) - r0;
-              end = static_cast<uint32_t>(r0 + i + 1) * static_cast<uint32_t>(p.per);
+              i = i < 0 ? static_cast<int>(r / static_cast<uint32_t>(p.per)) - r0 : i + 1;
+              start = static_cast<uint32_t>(r0 + i) * static_cast<uint32_t>(p.per);
+              end = start + static_cast<uint32_t>(p.per);
             }
           }
-          const uint32_t start = packed ? (i > 0 ? s.tok_end[i - 1] : before.tok) : end - static_cast<uint32_t>(p.per);
           const uint32_t t = r - start;
           if (t < s.add[i]) {
-            const uint32_t place = s.len[i] + t, pg = page_of(place, p), off = place - pg * page;
+            const uint32_t place = s.len[i] + t, pg = page_of(place, p);
             own_pos = static_cast<int>(place);
             if (s.served[i]) {
-              if (turn || id < 0 || pg != at) {
-                at = pg;
-                const uint32_t have = pages_of(s.len[i], p);
-                id = pg < have ? p.table[(r0 + i) * p.table_stride + pg]
-                               : fresh(s.take_end[i] - s.take[i] + pg - have);
-              }
-              if (id >= 0 && static_cast<uint32_t>(id) < p.pool) own_slot = static_cast<int>(id * page + off);
+              const uint32_t have = pages_of(s.len[i], p);
+              own = pg < have ? p.table + (r0 + i) * p.table_stride + pg
+                              : p.ring + ring_at(head0, s.take_end[i] - s.take[i] + pg - have);
+              own_off = place - pg * page;
             }
           }
         }
-        slot = make_int4(slot.y, slot.z, slot.w, own_slot);
+        where[0] = where[1], where[1] = where[2], where[2] = where[3], where[3] = own;
+        off[0] = off[1], off[1] = off[2], off[2] = off[3], off[3] = own_off;
         pos = make_int4(pos.y, pos.z, pos.w, own_pos);
       }
+      int id[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) id[e] = where[e] != nullptr ? *where[e] : -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        id[e] = static_cast<uint32_t>(id[e]) < p.pool ? static_cast<int>(id[e] * page + off[e]) : -1;
+      int4 slot = make_int4(id[0], id[1], id[2], id[3]);
       if (4 * g >= lo && 4 * g + 4 <= hi) {
         reinterpret_cast<int4*>(p.slots)[g] = slot;
         reinterpret_cast<int4*>(p.positions)[g] = pos;
@@ -232,7 +244,7 @@ __global__ void __launch_bounds__(kReq, 1) page_slots_kernel(const __grid_consta
       const int i = above(s.take_end, n_req, e);
       if (!s.served[i]) continue;
       const uint32_t j = e - (s.take_end[i] - s.take[i]);
-      p.table[(r0 + i) * p.table_stride + pages_of(s.len[i], p) + j] = fresh(e);
+      p.table[(r0 + i) * p.table_stride + pages_of(s.len[i], p) + j] = p.ring[ring_at(head0, e)];
     }
     // ---- pages given back
 #pragma unroll 1
