@@ -12,13 +12,14 @@ constexpr int kPagedBox = 64;     // most keys of one copy
 constexpr int kPagedCost = 1;     // what a unit costs besides its key tiles, in tiles
 constexpr int kPagedGrid = 152;   // CTAs at most: one an SM
 constexpr int kPagedWhole = 4;    // key tiles up to which units are not cut
+constexpr int kPagedGroup = 32;   // parts that are joined at once
 
 // A unit of work is a sequence, a K/V head and a block of its query rows. The
 // units of all sequences, each as long as its key tiles and kPagedCost, are one
 // line that is cut into as many equal runs as there are CTAs. Where a sequence can have
 // no more than kPagedWhole key tiles (the host knows what a row of the table holds, not
 // the lengths), a unit has a length of 1 and is not cut: then there is nothing to
-// join, no second kernel and no workspace.
+// join and no workspace.
 struct PagedParams {
   int B, H_kv;
   int R, s_q;              // query rows of a K/V head: (h / h_kv) * s_q, row x of token x % s_q
@@ -37,11 +38,16 @@ struct PagedParams {
   uint32_t q_box;          // bytes of a 64-column box of Q
   int grid;
   int whole;               // units are not cut
-  // Partial rows of units cut by a run's end: run c leaves slot 2 c for the
-  // unit it begins within and slot 2 c + 1 for the one it ends within.
+  // Partial rows of units cut by a run's end: run c leaves slot 2 c + 1 for the unit whose
+  // first part it has, and slot 2 c for the unit it begins within.
   float* part;             // [2 grid][rows a block][d_v]
   float* part_lse;         // [2 grid][rows a block], base 2
-  // {unit + 1 of slot 2 c or 0, 1 if the unit ends there, unit + 1 of slot 2 c + 1 or 0, 0}
+  // [grid][first group, later group, unit][half of the rows]: parts left so far (paged_count_in),
+  // at the first run of the group or unit
+  unsigned long long* words;
+  unsigned long long nonce;  // 48 bits, of this call
+  // Not null: the parts are joined by the kernel for that, which finds here {unit + 1 of
+  // slot 2 c or 0, 1 if the unit ends there, unit + 1 of slot 2 c + 1 or 0, 0}
   int4* runs;              // [grid]
   void* o;
   float* lse;

@@ -1,8 +1,10 @@
 // C entry points of the paged cache: block tables and slot maps, and the attention
 // over the pages. Argument checks, tensor maps and launch parameters.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <random>
 
 #include <cudaTypedefs.h>
 
@@ -76,10 +78,20 @@ int log2_of(int64_t n) {
   return s;
 }
 
-// Workspace: partial rows, their log-sums, the runs' records.
+// Workspace: partial rows, their log-sums, and the words that parts are counted in at
+// or the runs' records.
 size_t paged_bytes(int64_t R, int64_t d_v) {
   const size_t rows = static_cast<size_t>(2 * kPagedGrid) * static_cast<size_t>(paged_rows(static_cast<int>(R)));
-  return rows * (static_cast<size_t>(d_v) + 1) * sizeof(float) + kPagedGrid * sizeof(int4);
+  return rows * (static_cast<size_t>(d_v) + 1) * sizeof(float) + 6 * kPagedGrid * sizeof(unsigned long long);
+}
+
+// A number of 48 bits that no workspace holds by chance: from a random place on.
+unsigned long long next_nonce() {
+  static std::atomic<unsigned long long> next{[] {
+    std::random_device r;
+    return (static_cast<unsigned long long>(r()) << 32) ^ r();
+  }()};
+  return (next.fetch_add(1, std::memory_order_relaxed) & ((1ull << 48) - 1)) | (1ull << 47);
 }
 
 // Whether the units of sequences of up to `capacity` keys are left whole.
@@ -239,7 +251,13 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
   if (!whole) {
     p.part = static_cast<float*>(workspace);
     p.part_lse = p.part + static_cast<int64_t>(2 * kPagedGrid) * rows * d_v;
-    p.runs = reinterpret_cast<int4*>(p.part_lse + static_cast<int64_t>(2 * kPagedGrid) * rows);
+    void* rest = p.part_lse + static_cast<int64_t>(2 * kPagedGrid) * rows;
+    if (2 * b * h_kv * blocks < p.grid) {  // more than two parts a unit (paged_kernel.cuh)
+      p.runs = static_cast<int4*>(rest);
+    } else {
+      p.words = static_cast<unsigned long long*>(rest);
+      p.nonce = next_nonce();
+    }
   }
   p.o = o;
   p.lse = lse;
@@ -263,7 +281,7 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
   const int di = static_cast<int>(d_qk), dvi = static_cast<int>(d_v);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = bf16 ? launch_paged_bf16(di, dvi, m, p, st) : launch_paged_fp16(di, dvi, m, p, st);
-  if (e == cudaSuccess && !whole) e = launch_paged_join(bf16, dvi, p, st);
+  if (e == cudaSuccess && p.runs != nullptr) e = launch_paged_join(bf16, dvi, p, st);
   if (e != cudaSuccess) return fail(SDPA_ERR_CUDA, cudaGetErrorString(e));
   return SDPA_OK;
 }

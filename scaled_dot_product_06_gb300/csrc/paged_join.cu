@@ -1,4 +1,4 @@
-// Joins the partial rows of units that a run's end has cut (paged_kernel.cuh):
+// Joins the partial rows of units that runs' ends have cut into many (paged_kernel.cuh):
 //   L = log2 sum_s 2^L_s,  O = sum_s 2^(L_s - L) O_s,  LSE = L ln 2.
 // A block has one row of one run: it works if the run begins within a unit that
 // also ends in it, and then joins all slots of the unit, in the order of their

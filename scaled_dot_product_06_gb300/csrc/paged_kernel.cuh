@@ -23,9 +23,15 @@
 // The lengths are known on the device only. All units (sequence, K/V head, row
 // block) in a row, each as long as its key tiles, are one line, cut into equal
 // runs, one for each CTA: any mix of lengths ends at the same time on all SMs. A
-// unit that a run's end cuts leaves normalised fp32 rows and their log2-sum-exps,
-// at most two slots a CTA, joined by a second kernel (paged_join.cu); the others
-// are written as they are.
+// unit that a run's end cuts leaves normalised fp32 rows O_s and their log2-sum-exps
+// L_s, at most two slots a CTA, which are joined,
+//   L = log2 sum_s 2^L_s,  O = sum_s 2^(L_s - L) O_s,
+// in the order of the runs; the others are written as they are. Who leaves the last
+// of a unit's parts joins them where there are two a unit or fewer (by the units there
+// are): a kernel of its own for that (paged_join.cu) takes 6 us from the end of one to
+// the next call's first look at memory: 96 sequences of up to 5000 keys on one K/V
+// head 31.7 us for 33.6. Where there are more, that kernel does, with all SMs: one
+// sequence of 131072 keys, 8 K/V heads, 19 parts each, 81.3 us for 84.2.
 //
 // One persistent CTA an SM. Roles: two warpgroups of softmax threads (at NR = 8 and 16 they
 // take the key tiles in turns, each with a maximum, sum and O of its own, joined at
@@ -97,6 +103,7 @@ struct PagedItem {
   int k0;         // first key tile
   int len;        // keys of the sequence
   int slot;       // partial slot, or -1: the whole unit
+  int parts;      // of a cut unit: its first run, its runs << 16
 };
 
 // P^T, a key's rows side by side (MN-major): atoms of 8 keys as wide as the swizzle.
@@ -144,6 +151,34 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t phase, const E
   return ok;
 }
 
+// Of a cut unit: its first run, the group of parts that this CTA's is in, the words of
+// both (of a half of the rows).
+struct PagedParts {
+  int first, groups, from, n;
+  unsigned long long *word, *unit;
+};
+__device__ __forceinline__ PagedParts paged_parts(unsigned long long* words, int code, int half) {
+  const int first = code & 0xffff, parts = code >> 16;
+  const int group = (static_cast<int>(blockIdx.x) - first) / kPagedGroup, from = first + group * kPagedGroup;
+  return PagedParts{first, (parts + kPagedGroup - 1) / kPagedGroup, from, min(kPagedGroup, parts - group * kPagedGroup),
+                    words + 6 * from + (group == 0 ? 0 : 2) + half, words + 6 * first + 4 + half};
+}
+// A word of any former contents that parts are counted in at: nonce << 16 | count.
+// Made ready when the kernel starts, by each that will count itself in (one of them
+// succeeds; a compare-and-swap to count with would be tried again by all that come at
+// once, and one just before waits as long as the memory's queue is).
+__device__ __forceinline__ void paged_ready(unsigned long long* word, unsigned long long nonce) {
+  const unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+  if (old >> 16 != nonce) atomicCAS(word, old, nonce << 16);
+}
+// True for the last of `parts`, which leaves a 0 behind, so that a captured call,
+// whose nonce is the same in every replay, finds no count of the last replay.
+__device__ __forceinline__ bool paged_count_in(unsigned long long* word, int parts) {
+  const bool last = static_cast<int>((atomicAdd(word, 1ull) + 1) & 0xffff) == parts;
+  if (last) atomicExch(word, 0ull);
+  return last;
+}
+
 // Keys of a sequence, and its key tiles [lo, lo + n) that some new token sees.
 struct PagedSpan {
   int len, lo, n;
@@ -155,6 +190,93 @@ __device__ __forceinline__ PagedSpan paged_span(const PagedParams& p, int seqlen
   s.lo = first / kPagedTile;
   s.n = s.len > 0 ? (s.len + kPagedTile - 1) / kPagedTile - s.lo : 0;
   return s;
+}
+
+// The part of a cut unit has been written (by a warpgroup: half of the rows, or all of
+// them): the last to write one of a group of kPagedGroup parts joins the group, the
+// last to do that joins the groups. (A run may have the last part of a unit, a group by
+// itself, and the first of another: first groups and later ones have words of their
+// own.) False: a wait ran out, all leave. Not inlined: most units come without. o and
+// lse are those of the warpgroup's first row.
+template <int DV, bool BF16, int NR>
+__device__ __noinline__ bool paged_join(float* part, float* part_lse, unsigned long long* words, uint8_t* o, float* lse,
+                                        int code, int half, int bar_id, int col0, int live, bool ok, int* flag) {
+  constexpr int LANES = DV / 4, W = 4;  // lanes a row; parts fetched at once
+  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
+  const PagedParts c = paged_parts(words, code, half);
+  int from = c.from, n = c.n, step = 1;
+  unsigned long long* word = c.word;
+  bool final = c.groups == 1;
+#pragma unroll 1
+  for (;;) {
+    // what the warpgroup wrote is in memory
+    __threadfence();
+    if (!named_bar_and(bar_id, 128, ok)) {
+      named_bar_and(bar_id, 128, false);
+      return false;
+    }
+    if ((threadIdx.x & 127) == 0) *flag = paged_count_in(word, n) ? 1 : 0;
+    named_bar_and(bar_id, 128, true);
+    if (*reinterpret_cast<volatile int*>(flag) == 0) return true;
+    __threadfence();
+#pragma unroll 1
+    for (int e0 = w4; e0 < live; e0 += 8) {  // rows e0 and e0 + 4
+      float m2[2] = {SDPA_NEG_INF, SDPA_NEG_INF}, l2[2] = {0.f, 0.f};
+      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 1
+      for (int s0 = 0; s0 < n; s0 += W) {
+        float4 v[2][W];
+        float L[2][W];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const int run = from + min(s0 + i, n - 1) * step, e = min(e0 + 4 * r, live - 1);
+            const int64_t row = static_cast<int64_t>(2 * run + (run == c.first ? 1 : 0)) * NR + col0 + e;
+            L[r][i] = s0 + i < n ? __ldcg(part_lse + row) : SDPA_NEG_INF;
+            v[r][i] = __ldcg(reinterpret_cast<const float4*>(part + row * DV) + (lane & (LANES - 1)));
+          }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            // (a maximum that skips what is not a number: the weight then is none, and the row)
+            const float mn = fmaxf(m2[r], L[r][i]), base = mn == SDPA_NEG_INF ? 0.f : mn;
+            const float keep = ex2(m2[r] - base), w = ex2(L[r][i] - base);
+            const bool some = w > 0.f;
+            float4& a = acc[r];
+            m2[r] = mn;
+            l2[r] = fmaf(l2[r], keep, w);
+            a.x = fmaf(w, some ? v[r][i].x : 0.f, a.x * keep), a.y = fmaf(w, some ? v[r][i].y : 0.f, a.y * keep);
+            a.z = fmaf(w, some ? v[r][i].z : 0.f, a.z * keep), a.w = fmaf(w, some ? v[r][i].w : 0.f, a.w * keep);
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int e = e0 + 4 * r;
+        if (e >= live) break;
+        const float inv = l2[r] == 0.f ? 0.f : 1.f / l2[r], log_l = l2[r] == 0.f ? SDPA_NEG_INF : m2[r] + __log2f(l2[r]);
+        const float4 a = make_float4(acc[r].x * inv, acc[r].y * inv, acc[r].z * inv, acc[r].w * inv);
+        if (final) {
+          if (lane < LANES)
+            reinterpret_cast<uint2*>(o + e * (DV * 2))[lane] =
+                make_uint2(pack2<BF16>(a.x, a.y), pack2<BF16>(a.z, a.w));
+          if (lane == 0) lse[e] = log_l * kLn2;
+        } else {  // to the group's first slot
+          const int64_t row = static_cast<int64_t>(2 * from + (from == c.first ? 1 : 0)) * NR + col0 + e;
+          __syncwarp();
+          if (lane < LANES) reinterpret_cast<float4*>(part + row * DV)[lane] = a;
+          if (lane == 0) part_lse[row] = log_l;
+        }
+      }
+    }
+    if (final) return true;
+    from = c.first;
+    n = c.groups;
+    step = kPagedGroup;
+    word = c.unit;
+    final = true;
+  }
 }
 
 // How long a unit of the sequence is on the line.
@@ -180,7 +302,8 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
   uint32_t* scan = reinterpret_cast<uint32_t*>(tmem_slot + 8);     // [warps] sums
   int* items = reinterpret_cast<int*>(tmem_slot + 8 + 16);         // ring of 4, 8 words each
   int* sIds = items + 32;                                          // [producers][32] pages
-  static_assert(GB_COUNT * 8 + 96 + 128 + 256 <= 1024 && GB_COUNT % 2 == 0, "barrier region");
+  int* sFlag = sIds + 64;                                          // [warpgroups]
+  static_assert(GB_COUNT * 8 + 96 + 128 + 256 + 16 <= 1024 && GB_COUNT % 2 == 0, "barrier region");
   // [softmax warps][NC] values of rows. While maxima are exchanged, sMax holds each
   // warp's and sRow is its own; at a unit's end sRow holds each warp's sums and sMax is
   // its own. Between the two uses lies a barrier of the warpgroup.
@@ -243,6 +366,10 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
   const uint32_t each = total / gridDim.x, more = total - each * gridDim.x;
   const uint32_t run_lo = each * blockIdx.x + min(blockIdx.x, more);
   const uint32_t run_hi = run_lo + each + (blockIdx.x < more ? 1u : 0u);
+  auto run_of = [&](uint32_t at) -> int {  // the run that has a place of the line
+    const uint32_t longer = more * (each + 1);
+    return static_cast<int>(at < longer ? at / (each + 1) : more + (at - longer) / each);
+  };
   upto += before;
   if (run_lo < run_hi && run_lo >= upto - sum && run_lo < upto) {  // one thread of the CTA
     uint32_t at = run_lo - (upto - sum);
@@ -268,7 +395,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     const int4 a = *reinterpret_cast<const int4*>(items + (u & 3) * 8);
     const int4 b = *reinterpret_cast<const int4*>(items + (u & 3) * 8 + 4);
     auto one = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-    *it = PagedItem{one(a.x), one(a.y), one(a.z), one(a.w), one(b.x), one(b.y), one(b.z)};
+    *it = PagedItem{one(a.x), one(a.y), one(a.z), one(a.w), one(b.x), one(b.y), one(b.z), one(b.w)};
     return true;
   };
 
@@ -285,13 +412,13 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     int nt = 0, nu = 0, nq = 0;  // tiles copied, items told, items with keys so far
     int s = 0, round = 0;        // stage of the ring, and its uses
     bool ok = true;
-    int4 runs = make_int4(0, 0, 0, 0);
+    int4 record = make_int4(0, 0, 0, 0);
     auto tell = [&](const PagedItem& it) -> bool {
       if (!keys) return true;
       if (!free_of(GB_IE + (nu & 3), nu >> 2)) return false;
       if (lane == 0) {
         *reinterpret_cast<int4*>(items + (nu & 3) * 8) = make_int4(it.n, it.b, it.hk, it.rb);
-        *reinterpret_cast<int4*>(items + (nu & 3) * 8 + 4) = make_int4(it.k0, it.len, it.slot, 0);
+        *reinterpret_cast<int4*>(items + (nu & 3) * 8 + 4) = make_int4(it.k0, it.len, it.slot, it.parts);
         mbar_arrive(bar(GB_I + (nu & 3)));
       }
       __syncwarp();
@@ -300,7 +427,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     };
     uint32_t left = run_hi - run_lo;
     if (left > 0 && !paged_wait(bar(GB_START), 0, ec, kSiteFwdLoad)) left = 0;
-    int i = 0, unit = 0, pos = 0;
+    int i = 0, hk = 0, rb = 0, pos = 0;  // sequence, K/V head, row block; place in the unit
     PagedSpan sp{0, 0, 0}, sp_next{0, 0, 0};
     // A tile's copies are boxes of a page, of `box` keys each. Lane l has the page of
     // box ib + l of sequence is (in shared memory too, for the lane that copies), and of
@@ -319,8 +446,10 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
       i = l0 = start[0];
       sp = paged_span(p, start[2]);
       const int w = paged_weight(p, sp);
-      unit = start[1] / w;
+      const int unit = start[1] / w;
       pos = start[1] - unit * w;
+      hk = unit / p.row_blocks;
+      rb = unit - hk * p.row_blocks;
       // the first unit's pages at once, then the lengths of 32 sequences from l0 on, a
       // lane each, and of the 32 after them
       as = i;
@@ -343,19 +472,22 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
         PagedItem it;
         it.n = t1 - t0;
         it.b = i;
-        it.hk = unit / p.row_blocks;
-        it.rb = unit - it.hk * p.row_blocks;
+        it.hk = hk;
+        it.rb = rb;
         it.k0 = sp.lo + t0;
         it.len = sp.len;
         it.slot = -1;
-        const int id = i * units + unit + 1;
-        if (t0 > 0) {
-          it.slot = 2 * blockIdx.x;
-          runs.x = id;
-          runs.y = t1 == sp.n;
-        } else if (t1 < sp.n) {
-          it.slot = 2 * blockIdx.x + 1;
-          runs.z = id;
+        it.parts = 0;
+        if (t0 > 0 || t1 < sp.n) {  // cut: the runs with its first and its last tile
+          const uint32_t tile0 = run_hi - left - pos + kPagedCost;
+          const int from = run_of(tile0), to = run_of(tile0 + sp.n - 1);
+          it.slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
+          it.parts = from | (to - from + 1) << 16;
+          const int id = i * units + hk * p.row_blocks + rb + 1;
+          if (t0 > 0)
+            record.x = id, record.y = t1 == sp.n;
+          else
+            record.z = id;
         }
         if (!(ok = tell(it))) break;
         if (it.n > 0) {
@@ -374,7 +506,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
           // boxes with a key that some token sees: [first, end)
           const int seen = p.left < 0 ? 0 : max(0, sp.len - p.s_q - p.left);
           const int first = seen >> p.box_shift, end = (sp.len + p.box - 1) >> p.box_shift;
-          const bool again = unit + 1 < units;  // the next unit is of the same sequence
+          const bool again = hk + 1 < p.H_kv || rb + 1 < p.row_blocks;  // the next unit is of the same sequence
           for (int j = 0; j < it.n; ++j) {
             const int box0 = (it.k0 + j) * per_tile;
             const bool batch = j == 0 || box0 - ib == 32;  // another batch of pages
@@ -430,8 +562,12 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
       }
       left -= static_cast<uint32_t>(take);
       pos = 0;
-      if (++unit == units && left > 0) {
-        unit = 0;
+      if (++rb == p.row_blocks) {
+        rb = 0;
+        ++hk;
+      }
+      if (hk == p.H_kv && left > 0) {
+        hk = 0;
         ++i;
         if (i - l0 == 32) {
           l0 = i;
@@ -442,10 +578,10 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
         ahead_known = false;
       }
     }
-    // (the kernel that joins the partials may come: it waits for this one's end by itself)
+    if (keys && lane == 0 && p.runs != nullptr) p.runs[blockIdx.x] = record;
+    // (the next kernel may come: it waits for this one's end before it looks at memory)
     if (keys) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (ok) tell(PagedItem{-1, 0, 0, 0, 0, 0, 0});
-    if (keys && lane == 0 && !p.whole) p.runs[blockIdx.x] = runs;
+    if (ok) tell(PagedItem{-1, 0, 0, 0, 0, 0, 0, 0});
     // Every copy issued must land before the CTA can retire; on the healthy path they
     // did long ago.
     __syncwarp();
@@ -466,7 +602,28 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     uint32_t ph = 0;          // the stage's phase
     bool ok = true;
     PagedItem it;
-    for (int u = 0; (ok = next_item(u, &it)); ++u) {
+    if (p.words != nullptr && run_lo < run_hi) {
+      // While the first keys are on their way: the words that this run's parts will be
+      // counted in at, those of the unit that it ends within, and of the one that it begins
+      // within (where there are such).
+      ok = paged_wait(bar(GB_START), 0, ec, kSiteFwdMma);
+      if (ok && lane < 8) {
+        int code = static_cast<int>(blockIdx.x) | 1 << 16;
+        if (lane >= 4) {
+          const PagedSpan sp = paged_span(p, start[2]);
+          const int pos = start[1] % paged_weight(p, sp);
+          if (sp.n > 0) {
+            const int from = run_of(run_lo - pos + kPagedCost);
+            code = from | (run_of(run_lo - pos + kPagedCost + sp.n - 1) - from + 1) << 16;
+          }
+        }
+        const PagedParts c = paged_parts(p.words, code, lane & 1);
+        if (c.first <= static_cast<int>(blockIdx.x)) paged_ready((lane & 2) != 0 ? c.unit : c.word, p.nonce);
+        __threadfence();
+      }
+      __syncwarp();
+    }
+    for (int u = 0; ok && (ok = next_item(u, &it)); ++u) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(GB_IE + (u & 3)));
       if (it.n < 0) break;
@@ -655,6 +812,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
         l[e] = 0.f;
       }
       const int j0 = C::TURNS ? (g0 ^ t) & 1 : 0;
+      const bool ends = !C::TURNS || ((g0 + it.n - 1) & 1) == t;  // this warpgroup writes the rows
       for (int j = j0; j < it.n; j += C::OS) {
         const int g = g0 + j, key0 = (it.k0 + j) * BN, key = key0 + own_key;
         const bool first = j == j0;
@@ -670,15 +828,17 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
         const bool hidden = key0 + BN - 1 > last0 || (p.left >= 0 && key0 < last0 + p.s_q - 1 - p.left);
         bool out = false;  // a key that no row sees
         if (hidden) {
-          int tok = base % p.s_q;
-          out = true;
+          out = key > last0 + p.s_q - 1 || (p.left >= 0 && key < last0 - p.left);
+          if (p.s_q > 1) {  // or that only some tokens see
+            int tok = base % p.s_q;
 #pragma unroll
-          for (int e = 0; e < NC; ++e) {
-            if (key > last0 + tok || (p.left >= 0 && key < last0 + tok - p.left))
-              x[e] = hide;
-            else
-              out = false;
-            tok = tok + 1 == p.s_q ? 0 : tok + 1;
+            for (int e = 0; e < NC; ++e) {
+              if (key > last0 + tok || (p.left >= 0 && key < last0 + tok - p.left)) x[e] = hide;
+              tok = tok + 1 == p.s_q ? 0 : tok + 1;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < NC; ++e) x[e] = out ? hide : x[e];
           }
         }
         float most = SDPA_NEG_INF, least = -SDPA_NEG_INF;
@@ -770,7 +930,6 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
       }
       if (left_all) break;
       const bool both = C::TURNS && it.n > 1;
-      const bool ends = !C::TURNS || ((g0 + it.n - 1) & 1) == t;  // this warpgroup writes the rows
       if (j0 < it.n) {
         // ---- sums over the warp's keys: lane e gets row e's
 #pragma unroll
@@ -842,6 +1001,13 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < NC; ++e)
               if (has && e < live) dst[e * DV] = o[e];
+            // (in turns, either warpgroup has all rows)
+            if (p.runs == nullptr &&
+                !paged_join<DV, BF16, NR>(p.part, p.part_lse, p.words, static_cast<uint8_t*>(p.o) + row0 * (DV * 2),
+                                          p.lse + row0, it.parts, C::TURNS ? 0 : t, 1 + t, col0, live, ok, sFlag + t)) {
+              left_all = true;
+              break;
+            }
           } else {
             // two rows at a time: neighbouring lanes swap, and store two columns of a row each
             const bool odd = (lane & 1) != 0;

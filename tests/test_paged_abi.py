@@ -49,9 +49,9 @@ def test_refusals(lib):  # noqa: F811
 def test_workspace_size(lib):  # noqa: F811
     size = lib.sdpa_fwd_paged_workspace_size
     for h, h_kv, s_q, rows in ((8, 8, 1, 8), (16, 1, 1, 16), (32, 2, 1, 16), (32, 2, 2, 32), (33, 1, 1, 64), (64, 1, 8, 64)):
-        # two slots a CTA, rows of d_v + 1 floats, and 16 bytes a CTA
-        assert size(h, h_kv, s_q, 64, 64, 16, 33) == (304 * rows * 65 * 4 + 152 * 16 + 255) // 256 * 256
-        assert sdpa_fwd_paged_workspace_size(h, h_kv, s_q, 192, 128, 1024, 7) == (304 * rows * 129 * 4 + 2432 + 255) // 256 * 256
+        # two slots a CTA, rows of d_v + 1 floats, and six words a CTA
+        assert size(h, h_kv, s_q, 64, 64, 16, 33) == (304 * rows * 65 * 4 + 6 * 152 * 8 + 255) // 256 * 256
+        assert sdpa_fwd_paged_workspace_size(h, h_kv, s_q, 192, 128, 1024, 7) == (304 * rows * 129 * 4 + 6 * 152 * 8 + 255) // 256 * 256
         # up to four key tiles a sequence: nothing to join
         assert size(h, h_kv, s_q, 64, 64, 16, 32) == 0 and size(h, h_kv, s_q, 64, 64, 128, 0) == 0
     for bad in ((8, 3, 1, 64, 64, 16, 99), (8, 2, 1, 96, 96, 16, 99), (8, 2, 0, 64, 64, 16, 99), (8, 2, 1, 64, 64, 0, 99),
