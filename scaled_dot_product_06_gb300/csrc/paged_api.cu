@@ -2,9 +2,9 @@
 // over the pages. Argument checks, tensor maps and launch parameters.
 #include <algorithm>
 #include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdio>
-#include <random>
 
 #include <cudaTypedefs.h>
 
@@ -85,11 +85,15 @@ size_t paged_bytes(int64_t R, int64_t d_v) {
   return rows * (static_cast<size_t>(d_v) + 1) * sizeof(float) + 6 * kPagedGrid * sizeof(unsigned long long);
 }
 
-// A number of 48 bits that no workspace holds by chance: from a random place on.
+// A number of 48 bits that no workspace holds by chance: from a random place on (the
+// clock and an address, mixed by the finaliser of splitmix64), another for each call.
 unsigned long long next_nonce() {
   static std::atomic<unsigned long long> next{[] {
-    std::random_device r;
-    return (static_cast<unsigned long long>(r()) << 32) ^ r();
+    unsigned long long x = static_cast<unsigned long long>(std::chrono::steady_clock::now().time_since_epoch().count());
+    x ^= reinterpret_cast<uintptr_t>(&x) * 0x9E3779B97F4A7C15ull;
+    x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
+    x = (x ^ (x >> 27)) * 0x94D049BB133111EBull;
+    return x ^ (x >> 31);
   }()};
   return (next.fetch_add(1, std::memory_order_relaxed) & ((1ull << 48) - 1)) | (1ull << 47);
 }

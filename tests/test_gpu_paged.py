@@ -52,6 +52,11 @@ CASES = [
     (3, 8, 2, 3, [1000, 130, 2], 32, 128, 128, "fp16", 25.0, 127, False),
     (2, 40, 1, 2, [3001, 640], 128, 192, 128, "bf16", 0.0, 1000, False),
     (2, 4, 2, 6, [300, 5], 16, 64, 64, "bf16", 0.0, 2, False),
+    # many units, one of them in so many parts that they are joined in groups
+    (90, 4, 1, 1, [1] * 45 + [40000] + [3] * 44, 16, 128, 128, "bf16", 0.0, -1, False),
+    (80, 40, 1, 1, [130] * 79 + [30000], 64, 64, 64, "fp16", 0.0, -1, True),    # by halves of the rows
+    (80, 16, 1, 1, [20000] + [0, 300] * 39 + [5000], 128, 192, 128, "bf16", 0.0, -1, False),
+    (100, 2, 1, 2, [(i * 331) % 2500 for i in range(100)], 32, 128, 128, "bf16", 30.0, 900, False),
 ]
 
 
@@ -238,31 +243,54 @@ def test_pools_past_32_bits():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-def test_captured_graphs_that_share_a_workspace():
-    """Two captured calls with one workspace, replayed in turn on lengths that change."""
-    need = sdpa_fwd_paged_workspace_size(16, 2, 1, 128, 128, 16, 100)
-    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
-    xs = [make(b, 16, 2, 1, [n] * b, 16, 128, 128, torch.bfloat16, seed=b, garbage=False)
-          for b, n in ((3, 2000), (1, 6000))]
+@pytest.mark.parametrize("batches", [(3, 1), (80, 50)], ids=["many parts", "few parts"])
+def test_captured_graphs_that_share_a_workspace(batches):
+    """Two captured calls with one workspace, replayed in turn on lengths that change,
+    and that a copy within the graph brings."""
+    page, h_kv = 16, 2
+    lens = [6000 // b + 600 for b in batches]
+    xs = [make(b, 16, h_kv, 1, [n] * b, page, 128, 128, torch.bfloat16, seed=b, garbage=False)
+          for b, n in zip(batches, lens)]
+    ws = torch.full((max(sdpa_fwd_paged_workspace_size(16, h_kv, 1, 128, 128, page, x["block_table"].shape[1])
+                         for x in xs),), 0xFF, dtype=torch.uint8, device="cuda")
     gs = [cuda(x) for x in xs]
+    news = [g["seqlens_k"].clone() for g in gs]
     graphs, outs = [], []
-    for g in gs:
+    for g, new in zip(gs, news):
         sdpa_fwd_paged(**g, workspace=ws)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
+            g["seqlens_k"].copy_(new)
             outs.append(sdpa_fwd_paged(**g, workspace=ws))
         graphs.append(graph)
-    for step in range(4):
-        for x, g, graph, out in zip(xs, gs, graphs, outs):
-            n = [max(0, int(v) - 431 * step * (i + 1)) for i, v in enumerate([int(x["k_pages"].shape[0] * 16 // len(
-                x["seqlens_k"]) - 100)] * len(x["seqlens_k"]))]
-            g["seqlens_k"].copy_(torch.tensor(n, dtype=torch.int32))
+    rng = torch.Generator().manual_seed(3)
+    for step in range(8):
+        for g, new, graph, out, n in zip(gs, news, graphs, outs, lens):
+            new.copy_(torch.randint(0, n + 1, new.shape, generator=rng).to(torch.int32))
             graph.replay()
+            if step % 2:
+                graph.replay()
             want = sdpa_fwd_paged(**g)
             assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
-            ws.fill_(0xFF)
+            if step % 3 == 0:
+                ws.random_(0, 256)
     assert sdpa_device_error() == 0
+
+
+@pytest.mark.parametrize("c", [CASES[15], CASES[25], CASES[26], CASES[28]], ids=case_id)
+def test_workspaces_of_any_contents(c):
+    """What the workspace holds, another call's leftovers or anything, changes no bit."""
+    x = cuda(inputs(c, garbage=False))
+    kw = dict(softcap=c[9], window_left=c[10])
+    want = sdpa_fwd_paged(**x, **kw)
+    need = sdpa_fwd_paged_workspace_size(c[1], c[2], c[3], c[6], c[7], c[5], x["block_table"].shape[1])
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for fill in (0, 0xFF, 0x80, None, None):
+        if fill is not None:
+            ws.fill_(fill)
+        got = sdpa_fwd_paged(**x, **kw, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_two_streams_at_once():
