@@ -586,7 +586,6 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     // did long ago.
     __syncwarp();
     if (*abort_flag) {
-      
 #pragma unroll 1
       for (int b = 0; b < C::Q_BUFS; ++b)
         if (nq > b) mbar_wait(bar(GB_Q + b), ((nq - 1 - b) / C::Q_BUFS) & 1, ec, kSiteDrain, false);

@@ -2,6 +2,7 @@
 element by element; bounds in paged_ref."""
 from __future__ import annotations
 
+import concurrent.futures
 import math
 
 import pytest
@@ -304,6 +305,48 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_captured_calls_that_allocate():
+    """Captured calls without a given workspace: each one's is handed on within the graph."""
+    lens = [700, 3000, 1, 640, 2048, 999]
+    xs = [cuda(make(6, 8, 2, 1, lens, 16, 64, 64, torch.float16, seed=s, garbage=False)) for s in range(2)]
+    need = sdpa_fwd_paged_workspace_size(8, 2, 1, 64, 64, 16, xs[0]["block_table"].shape[1])
+    assert need > 0
+    sdpa_fwd_paged(**xs[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = []
+        for x in xs:
+            outs.append(sdpa_fwd_paged(**x))
+            torch.empty(need, dtype=torch.uint8, device="cuda").fill_(0xA5)
+    for step in range(6):
+        for x in xs:
+            x["seqlens_k"].copy_(torch.tensor([max(n - 37 * step, 0) for n in lens], dtype=torch.int32))
+        graph.replay()
+        for x, out in zip(xs, outs):
+            want = sdpa_fwd_paged(**x)
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_two_threads_at_once():
+    x = [cuda(make(8, 8, 2, 1, [4000 - 400 * i for i in range(8)], 16, 128, 128, torch.bfloat16, seed=s))
+         for s in range(2)]
+    want = [sdpa_fwd_paged(**g) for g in x]
+    torch.cuda.synchronize()
+
+    def calls(i):
+        stream = torch.cuda.Stream()
+        return all(torch.equal(a, b) for _ in range(40) for a, b in zip(finished(i, stream), want[i]))
+
+    def finished(i, stream):
+        got = sdpa_fwd_paged(**x[i], stream=stream)
+        stream.synchronize()
+        return got
+
+    with concurrent.futures.ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(calls, range(2)))
 
 
 def test_equals_the_contiguous_cache():
