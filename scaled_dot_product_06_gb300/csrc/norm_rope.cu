@@ -17,12 +17,19 @@
 // copies, each thread its own 16 bytes and reading back only those (no
 // barrier), so the loads in flight hold no registers: with plain loads, four
 // rows a thread ahead of their use, a call at b1 s16384 h32 + 2 x 4, d = 128
-// took 74 us (68% of the copy rate; now 59 us, 85%) and its backward at b4
+// took 74 us (68% of the copy rate; now 57 us, 89%) and its backward at b4
 // s2048, 3 x 16 heads, 113 us (36%; now 65 us, 62%: no unit is near its limit,
 // but a warp takes one row at a time, and wait for the copy, the partner's
 // elements, four rounds of two sums' shuffles, the root and the store follow one
 // another, 24 warps an SM). Shorter walks than 16 heads lose more to the angles
 // than they gain in grain: 65 us at 8, 72 us at 4, for 60 us of the kernel alone.
+//
+// Into pages (kv_slots), 8191 tokens of 16 + 2 x 4 heads, d = 192 / 128, take 31.3 us
+// (68% of the copy rate): a row of 192 leaves 8 lanes of its warp idle, and
+// instructions are issued in 73% of the cycles. The divisions by what the host knows
+// (tokens a sequence, blocks of tokens, rows a page) are multiplications: 31.9 us
+// with the compiler's. Two rows a warp, 12 lanes with two chunks each: 32.8 us, and 53.2
+// for 47.5 of 16 + 2 x 16 heads (80 registers, 24 warps an SM).
 #include <algorithm>
 
 #include "common.cuh"
@@ -162,6 +169,9 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// n / d, n < 2^31
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divider& d) { return (__umulhi(n, d.m) + n) >> d.s; }
+
 // A warp's walk: work unit u of its kind is head segment u / n_tb of token block
 // u % n_tb (RPW consecutive tokens, one a lane group).
 struct Unit {
@@ -172,15 +182,14 @@ struct Unit {
 template <int RPW>
 __device__ __forceinline__ Unit unit_of(const NormRopeParams& p, const RowKind& k, uint32_t u, int sub,
                                         bool lane_ok) {
-  const uint32_t n_tb = static_cast<uint32_t>((p.tokens + RPW - 1) / RPW);
-  const uint32_t sg = u / n_tb, tb = u - sg * n_tb;
+  const uint32_t sg = quotient(u, p.n_tb), tb = u - sg * p.n_tb.d;
   Unit r;
   const uint32_t tok = tb * RPW + sub;
   r.live = lane_ok && tok < p.tokens;
   const uint32_t tk = r.live ? tok : 0;
   r.token = tk;
-  r.b = static_cast<int>(tk / static_cast<uint32_t>(p.s));
-  r.t = static_cast<int>(tk - static_cast<uint32_t>(r.b) * static_cast<uint32_t>(p.s));
+  r.b = static_cast<int>(quotient(tk, p.s));
+  r.t = static_cast<int>(tk - static_cast<uint32_t>(r.b) * p.s.d);
   r.h0 = static_cast<int>(sg) * p.seg;
   r.n = min(p.seg, k.heads - r.h0);
   return r;
@@ -210,8 +219,9 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_fwd_kernel(const __grid
   if (k.cached) {
     if (p.kv_slots != nullptr) {
       const uint32_t slot = un.live ? static_cast<uint32_t>(__ldg(p.kv_slots + un.token)) : 0u;
-      outer = slot / p.page_size;
-      row = slot % p.page_size;
+      const uint32_t page = quotient(slot, p.page_size);
+      outer = page;
+      row = slot - page * p.page_size.d;
       store = un.live && slot < p.n_slots;  // (negative slots are large ones here)
     } else {
       row += un.live ? __ldg(p.kv_rows + un.b) : 0;
@@ -427,6 +437,7 @@ int norm_rope_plan(NormRopeParams* p, bool backward) {
   constexpr int W = kThreads / 32;
   const int rpw = p->d == 64 ? RowCfg<64>::RPW : (p->d == 128 ? RowCfg<128>::RPW : RowCfg<192>::RPW);
   const int64_t n_tb = (p->tokens + rpw - 1) / rpw;
+  p->n_tb = divider(n_tb > 0 ? n_tb : 1);
   // heads a warp walks: sixteen, or the largest power of two below that leaves
   // 32 warps an SM
   auto warps = [&](int seg) {

@@ -13,6 +13,19 @@ struct RowSet {
   int64_t sb, st, sh;
 };
 
+// Division of numbers below 2^31 by one that the host knows, by a multiplication
+// (Granlund and Montgomery, 1994): with 2^s >= d > 2^(s - 1) and m = floor(2^32 (2^s - d) / d)
+// + 1, n / d = (floor(m n / 2^32) + n) / 2^s.
+struct Divider {
+  uint32_t d, m, s;
+};
+inline Divider divider(int64_t d) {
+  uint32_t s = 0;
+  while ((int64_t{1} << s) < d) ++s;
+  const uint64_t rest = (uint64_t{1} << s) - static_cast<uint64_t>(d);
+  return Divider{static_cast<uint32_t>(d), static_cast<uint32_t>((rest << 32) / static_cast<uint64_t>(d) + 1), s};
+}
+
 // One kind of row (queries, keys or values) of a call. The `token` side is the
 // projection's layout, the `head` side the attention's (its sb / st / sh are
 // the strides of batch, row and head there).
@@ -30,9 +43,11 @@ struct NormRopeParams {
   RowKind kind[3];
   int n_kinds;
   int64_t tokens;  // b * s
-  int s;
+  Divider s;
+  Divider n_tb;    // blocks of tokens (norm_rope_plan)
   int d, rot, interleaved;
   int seg;         // heads a work unit walks (norm_rope_plan)
+  int paired;      // the walk of a token's keys goes on with its values (forward)
   float eps;
   int weight_fp32;       // weights are fp32 (else the io type)
   const float* cos;      // [n_pos][rot / 2]
@@ -44,7 +59,7 @@ struct NormRopeParams {
   // pages instead of caches: token t's row is row slot % page_size of page
   // slot / page_size (head.sb is then the stride of the pages)
   const int* kv_slots;   // [tokens] or null
-  uint32_t page_size;
+  Divider page_size;
   uint32_t n_slots;      // rows of all pages
   // backward: head = dy, token = dx, x = the forward's input; fp32 partial weight
   // gradients, one row of d per block of kinds 0 and 1

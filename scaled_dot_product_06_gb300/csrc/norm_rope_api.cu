@@ -1,5 +1,6 @@
 // C entry points of the query/key norm with the position rotation: argument
 // checks and launch parameters.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -73,7 +74,7 @@ void fill_common(NormRopeParams* p, int64_t b, int64_t s, int64_t d, int64_t rot
                  const float* cos, const float* sin, int64_t n_pos, const int32_t* positions, int weight_fp32,
                  float eps) {
   p->tokens = b * s;
-  p->s = static_cast<int>(s);
+  p->s = divider(std::max<int64_t>(s, 1));
   p->d = static_cast<int>(d);
   p->rot = static_cast<int>(rot);
   p->interleaved = interleaved ? 1 : 0;
@@ -126,7 +127,7 @@ sdpa_status_t forward(int64_t b, int64_t s, int64_t h, int64_t h_kv, int64_t d, 
   p.kv_rows = to.kv_rows;
   p.cache_rows = to.cache_rows;
   p.kv_slots = to.kv_slots;
-  p.page_size = static_cast<uint32_t>(to.page_size);
+  if (paged) p.page_size = divider(to.page_size);
   p.n_slots = static_cast<uint32_t>(to.n_pages * to.page_size);
   const int hi = static_cast<int>(h), hk = static_cast<int>(h_kv), di = static_cast<int>(d);
   auto kv_to = [&](const sdpa_rows_t* r) { return to_kv ? row_set(r, kv_outer, kv_out_rows, h_kv) : RowSet{}; };
