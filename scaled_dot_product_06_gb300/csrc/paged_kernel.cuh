@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
   for (int i = tid; i < C::Q_BUFS * C::Q_BYTES / 16; i += C::THREADS)
     reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
-  // (launched while the kernel before runs out: from here on its memory is looked at)
+  // (launched while the kernel before runs out: from here on its memory is looked at, by loads
+  // that are not the read-only ones, which the compiler may put ahead of this)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- this CTA's run: [lo, hi) of the line of all units
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
   uint32_t sum = 0;
 #pragma unroll 1
   for (int i = tid * per; i < min(p.B, (tid + 1) * per); ++i)
-    sum += p.whole ? 1u : static_cast<uint32_t>(paged_weight(p, paged_span(p, __ldg(p.seqlen + i))));
+    sum += p.whole ? 1u : static_cast<uint32_t>(paged_weight(p, paged_span(p, p.seqlen[i])));
   sum *= static_cast<uint32_t>(units);
   uint32_t upto = sum;
 #pragma unroll
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     int i = tid * per;
 #pragma unroll 1
     for (;; ++i) {
-      const int len = __ldg(p.seqlen + i);
+      const int len = p.seqlen[i];
       const uint32_t w = static_cast<uint32_t>(paged_weight(p, paged_span(p, len))) * units;
       if (at < w) {
         start[2] = len;
@@ -437,10 +438,10 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     int* own_ids = sIds + (keys ? 0 : 32);
     auto pages_of = [&](int i, int len, int b0) {  // (looked at, and held inside the pool, where it is used)
       const int key = (b0 + lane) << p.box_shift;
-      return key < len ? __ldg(p.table + i * p.table_stride + (key >> p.page_shift)) : 0;
+      return key < len ? p.table[i * p.table_stride + (key >> p.page_shift)] : 0;
     };
     int l0 = 0, lens = 0, lens_ahead = 0;
-    auto length = [&](int i) { return i < p.B ? __ldg(p.seqlen + i) : 0; };
+    auto length = [&](int i) { return i < p.B ? p.seqlen[i] : 0; };
     auto first_tile = [&]() { return sp.lo + (p.whole ? 0 : max(pos - kPagedCost, 0)); };
     if (left > 0) {
       i = l0 = start[0];
@@ -683,7 +684,6 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
         if (((lo | hi) & 15) != 0) {
           uint8_t* v = smem + C::OFF_V + s * C::V_BYTES;
           const int front = lo & 15, rows = front + (-hi & 15);
-            #pragma unroll 1
 #pragma unroll 1
           for (int e = lane; e < rows * 8; e += 32) {
             const int r = e / 8 < front ? lo - front + e / 8 : hi + e / 8 - front;
