@@ -96,8 +96,8 @@ __device__ __forceinline__ Turn load_turn(const NormRopeParams& p, bool rotate, 
     const float* cr = p.cos + pos * half;
     const float* sr = p.sin + pos * half;
     if (p.interleaved) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(cr) + l);
-      const float4 s = __ldg(reinterpret_cast<const float4*>(sr) + l);
+      const float4 c = reinterpret_cast<const float4*>(cr)[l];
+      const float4 s = reinterpret_cast<const float4*>(sr)[l];
       const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -111,8 +111,8 @@ __device__ __forceinline__ Turn load_turn(const NormRopeParams& p, bool rotate, 
       r.partner = lane + (second ? -half / 8 : half / 8);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(cr + i0) + q);
-        const float4 s = __ldg(reinterpret_cast<const float4*>(sr + i0) + q);
+        const float4 c = reinterpret_cast<const float4*>(cr + i0)[q];
+        const float4 s = reinterpret_cast<const float4*>(sr + i0)[q];
         const float m = second ? 1.f : -1.f;
         r.c[4 * q] = c.x, r.c[4 * q + 1] = c.y, r.c[4 * q + 2] = c.z, r.c[4 * q + 3] = c.w;
         r.s[4 * q] = m * s.x, r.s[4 * q + 1] = m * s.y, r.s[4 * q + 2] = m * s.z, r.s[4 * q + 3] = m * s.w;
@@ -145,10 +145,10 @@ __device__ __forceinline__ void load_weight(const NormRopeParams& p, const RowKi
   if (k.weight == nullptr || !live) return;
   if (p.weight_fp32) {
     const float4* w4 = static_cast<const float4*>(k.weight) + 2 * l;
-    const float4 a = __ldg(w4), b = __ldg(w4 + 1);
+    const float4 a = w4[0], b = w4[1];
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   } else {
-    unpack8<BF16>(__ldg(static_cast<const uint4*>(k.weight) + l), w);
+    unpack8<BF16>(static_cast<const uint4*>(k.weight)[l], w);
   }
 }
 
@@ -203,6 +203,11 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_fwd_kernel(const __grid
   __shared__ uint4 ring[kRing][kThreads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / C::L, l = lane - sub * C::L;  // row of the warp, lane of the row
+  // Launched while the kernel before runs out (256 decoding tokens of 32 + 2 x 8 heads 3.9
+  // us for 4.4): memory is looked at from here on, by loads that are not the read-only
+  // ones, which the compiler may put ahead of this. The kernel behind is not
+  // called up early: its blocks beside this one's took 9.4 us for 8.0 of 1000 tokens d192.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const RowKind& k = p.kind[kind_of_block(p, blockIdx.x)];
   const uint32_t u = (blockIdx.x - k.block0) * C::WARPS + warp;
   if (u >= k.units) return;  // whole warps
@@ -218,19 +223,19 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_fwd_kernel(const __grid
   bool store = un.live;
   if (k.cached) {
     if (p.kv_slots != nullptr) {
-      const uint32_t slot = un.live ? static_cast<uint32_t>(__ldg(p.kv_slots + un.token)) : 0u;
+      const uint32_t slot = un.live ? static_cast<uint32_t>(p.kv_slots[un.token]) : 0u;
       const uint32_t page = quotient(slot, p.page_size);
       outer = page;
       row = slot - page * p.page_size.d;
       store = un.live && slot < p.n_slots;  // (negative slots are large ones here)
     } else {
-      row += un.live ? __ldg(p.kv_rows + un.b) : 0;
+      row += un.live ? p.kv_rows[un.b] : 0;
       store = un.live && row >= 0 && row < p.cache_rows;
     }
   }
   uint16_t* dst = static_cast<uint16_t*>(k.head.ptr) + outer * k.head.sb + row * k.head.st + un.h0 * k.head.sh + 8 * l;
   const bool normed = k.weight != nullptr, rotate = k.rotate != 0;
-  const int64_t pos = (rotate && p.positions != nullptr && un.live) ? __ldg(p.positions + un.token) : un.t;
+  const int64_t pos = (rotate && p.positions != nullptr && un.live) ? p.positions[un.token] : un.t;
   float cw[8], sw[8];  // the angles times the weights of the element and of its partner
   load_weight<BF16>(p, k, l, un.live, cw);
   const Turn turn = load_turn(p, rotate && un.live, pos, l, lane);
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_bwd_kernel(const __grid
 #pragma unroll 1
   for (uint32_t u = u0; u < k.units; u += step) {
     const Unit un = unit_of<C::RPW>(p, k, u, sub, lane_ok);
-    const int64_t pos = (rotate && p.positions != nullptr && un.live) ? __ldg(p.positions + un.token) : un.t;
+    const int64_t pos = (rotate && p.positions != nullptr && un.live) ? p.positions[un.token] : un.t;
     const Turn turn = load_turn(p, rotate && un.live, pos, l, lane);
     uint16_t* dst = static_cast<uint16_t*>(k.token.ptr) + un.b * k.token.sb + un.t * k.token.st +
                     un.h0 * k.token.sh + 8 * l;
@@ -418,8 +423,16 @@ __global__ void __launch_bounds__(1024) dw_reduce_kernel(const float* __restrict
 
 template <bool BF16, int D>
 cudaError_t launch_fwd_d(const NormRopeParams& p, int blocks, cudaStream_t st) {
-  norm_rope_fwd_kernel<BF16, D><<<blocks, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_rope_fwd_kernel<BF16, D>, p);
 }
 
 template <bool BF16, int D>
