@@ -123,3 +123,64 @@ def test_serving_loop_equals_the_whole_sequences():
     head, tail = span.tolist()
     owned += [int(ring[j % POOL]) for j in range(head, tail)]
     assert sorted(owned) == list(range(POOL))
+
+
+def test_captured_on_streams_that_fork_and_join():
+    """Slots on one stream, the queries' copy on another, norm and attention behind both;
+    replays equal the calls one by one."""
+    dt, b, h, h_kv, d, page, pool = torch.float16, 5, 8, 2, 64, 16, 400
+    g = torch.Generator().manual_seed(2)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g).to(dt).cuda()
+
+    q0, k, v = randn(b, 1, h, d), randn(b, 1, h_kv, d), randn(b, 1, h_kv, d)
+    ang = torch.rand(2000, d // 2, generator=g).cuda()
+    cos, sin = ang.cos(), ang.sin()
+    pages = [randn(pool, h_kv, page, d) for _ in range(2)]
+    ring = torch.randperm(pool, generator=g).to(torch.int32).cuda()
+    new = torch.tensor([1, 1, 0, 1, 1], dtype=torch.int32).cuda()
+    first = torch.tensor([900, 0, 33, 15, 640], dtype=torch.int32).cuda()
+
+    def state():
+        table = torch.full((b, 64), -1, dtype=torch.int32, device="cuda")
+        used = 0
+        for i, n in enumerate(first.tolist()):
+            own = -(-n // page)
+            table[i, :own] = ring[used:used + own]
+            used += own
+        span = torch.tensor([used, pool], dtype=torch.int64, device="cuda")
+        return dict(table=table, ring=ring.clone(), span=span, lens=first.clone(), q=torch.zeros_like(q0),
+                    kp=pages[0].clone(), vp=pages[1].clone())
+
+    def slots_of(s):
+        return sdpa_page_slots(s["lens"], new, s["table"], s["ring"], s["span"], page, width=1, seqlens_out=s["lens"],
+                               free_range_out=s["span"])[:2]
+
+    def attend(s, slots, positions):
+        q1, _, _ = sdpa_qk_norm_rope(s["q"], k, cos, sin, v=v, positions=positions, kv_slots=slots, k_out=s["kp"],
+                                     v_out=s["vp"])
+        return sdpa_fwd_paged(q1, s["kp"], s["vp"], s["table"], s["lens"])
+
+    a, e = state(), state()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        for s in side:
+            s.wait_stream(main)
+        with torch.cuda.stream(side[0]):
+            slots, positions = slots_of(a)
+        with torch.cuda.stream(side[1]):
+            a["q"].copy_(q0)
+        for s in side:
+            main.wait_stream(s)
+        got = attend(a, slots, positions)
+    for _ in range(20):
+        graph.replay()
+        e["q"].copy_(q0)
+        want = attend(e, *slots_of(e))
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert all(torch.equal(a[n], e[n]) for n in a)
