@@ -73,10 +73,19 @@ struct PagedCfg {
   static constexpr int P_BUFS = TURNS ? 2 : 1;
   // barriers and so on; two rows of NC floats a softmax warp; statistics handed over
   static constexpr int MISC = 1024 + SOFT / 32 * NC * 8 + (TURNS ? 4 * NR * 8 : 0);
-  static constexpr int Q_BUFS = Q_BYTES > 16384 ? 1 : 2;
-  static constexpr int AVAIL = 227 * 1024 - 1024 - Q_BUFS * Q_BYTES - P_BUFS * P_BYTES - MISC;
-  static constexpr int FIT = AVAIL / (K_BYTES + V_BYTES);
+  // Few rows: a unit's queries come with its first keys, into as many buffers as there
+  // are stages. (A stage's wait for tile t - ST is then one for the queries' buffer: the ST - 1
+  // units between have a tile each, so that of the unit which had it lies no later.) With a
+  // ring of two and barriers of their own, as for more rows, whose buffers are larger, 256
+  // sequences of up to 100 keys on 8 K/V heads took 21.3 us for 19.5: their many short units
+  // are bound by the keys' producer and by the ends of units.
+  static constexpr bool Q_WITH_K = TURNS;
+  static constexpr int AVAIL = 227 * 1024 - 1024 - P_BUFS * P_BYTES - MISC;
+  static constexpr int Q_RING = Q_BYTES > 16384 ? 1 : 2;
+  static constexpr int FIT = Q_WITH_K ? AVAIL / (K_BYTES + V_BYTES + Q_BYTES)
+                                      : (AVAIL - Q_RING * Q_BYTES) / (K_BYTES + V_BYTES);
   static constexpr int ST = FIT > 6 ? 6 : FIT;
+  static constexpr int Q_BUFS = Q_WITH_K ? ST : Q_RING;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + ST * K_BYTES;
   static constexpr int OFF_Q = OFF_V + ST * V_BYTES;
@@ -492,18 +501,21 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
         }
         if (!(ok = tell(it))) break;
         if (it.n > 0) {
-          if (keys) {
-            const int qb = nq % C::Q_BUFS;
+          const int qb = nq % C::Q_BUFS;
+          auto copy_q = [&](uint32_t b) {
+#pragma unroll
+            for (int c = 0; c < DQK / 64; ++c)
+              tma_load_4d(sQ + qb * C::Q_BYTES + c * N * 128, &tmQ, b, c * 64, it.rb * NR, it.b, it.hk);
+          };
+          if (!C::Q_WITH_K && keys) {
             if (!(ok = free_of(GB_QE + qb, nq / C::Q_BUFS))) break;
             if (elect_one_sync()) {
               mbar_arrive_expect_tx(bar(GB_Q + qb), (DQK / 64) * p.q_box);
-#pragma unroll
-              for (int c = 0; c < DQK / 64; ++c)
-                tma_load_4d(sQ + qb * C::Q_BYTES + c * N * 128, &tmQ, bar(GB_Q + qb), c * 64, it.rb * NR, it.b, it.hk);
+              copy_q(bar(GB_Q + qb));
             }
             __syncwarp();
-            ++nq;
           }
+          ++nq;
           // boxes with a key that some token sees: [first, end)
           const int seen = p.left < 0 ? 0 : max(0, sp.len - p.s_q - p.left);
           const int first = seen >> p.box_shift, end = (sp.len + p.box - 1) >> p.box_shift;
@@ -523,7 +535,9 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
             const int lo = max(box0, first), hi = min(box0 + per_tile, end);
             if (elect_one_sync()) {
               const uint32_t b = bar(full + s), rows = static_cast<uint32_t>(p.box) * 128u;  // bytes of a box
-              mbar_arrive_expect_tx(b, static_cast<uint32_t>(hi - lo) * rows * width);
+              const bool with_q = C::Q_WITH_K && keys && j == 0;
+              mbar_arrive_expect_tx(b, static_cast<uint32_t>(hi - lo) * rows * width + (with_q ? (DQK / 64) * p.q_box : 0u));
+              if (with_q) copy_q(b);
               uint32_t dst = ring + s * stage_bytes + static_cast<uint32_t>(lo - box0) * rows;
 #pragma unroll 1
               for (int x = lo; x < hi; ++x, dst += rows) {
@@ -542,17 +556,15 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
             if (batch) {
               // the batch after this one: of this unit, of the next one of the sequence,
               // or of the next sequence
-              if (!ahead_known) {
-                sp_next = span_of(i + 1);
-                ahead_known = true;
-              }
               if ((it.k0 + it.n) * per_tile > box0 + 32) {
                 as = i, ab = box0 + 32;
                 ids_ahead = pages_of(i, sp.len, ab);
               } else if (again && sp.lo * per_tile != box0) {
                 as = i, ab = sp.lo * per_tile;
                 ids_ahead = pages_of(i, sp.len, ab);
-              } else if (i + 1 < p.B && (as != i + 1 || ab != sp_next.lo * per_tile)) {
+              } else if (as != i + 1 && i + 1 < p.B) {
+                sp_next = span_of(i + 1);
+                ahead_known = true;
                 as = i + 1, ab = sp_next.lo * per_tile;
                 ids_ahead = pages_of(i + 1, sp_next.len, ab);
               }
@@ -589,7 +601,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     if (*abort_flag) {
 #pragma unroll 1
       for (int b = 0; b < C::Q_BUFS; ++b)
-        if (nq > b) mbar_wait(bar(GB_Q + b), ((nq - 1 - b) / C::Q_BUFS) & 1, ec, kSiteDrain, false);
+        if (!C::Q_WITH_K && keys && nq > b) mbar_wait(bar(GB_Q + b), ((nq - 1 - b) / C::Q_BUFS) & 1, ec, kSiteDrain, false);
 #pragma unroll 1
       for (int s = 0; s < ST; ++s)
         if (nt > s) mbar_wait(bar(full + s), ((nt - 1 - s) / ST) & 1, ec, kSiteDrain, false);
@@ -629,7 +641,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
       if (it.n < 0) break;
       if (it.n == 0) continue;
       const int qb = q % C::Q_BUFS;
-      if (!(ok = paged_wait(bar(GB_Q + qb), (q / C::Q_BUFS) & 1, ec, kSiteFwdMma))) break;
+      if (!C::Q_WITH_K && !(ok = paged_wait(bar(GB_Q + qb), (q / C::Q_BUFS) & 1, ec, kSiteFwdMma))) break;
       const uint64_t dQ = desc_adv(dQ0, qb * C::Q_BYTES);
       for (int j = 0; j < it.n; ++j, ++g) {
         // S's buffer: P of the tile before the last one, formed from it, is there
@@ -644,7 +656,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
                     desc_adv(dQ, (kk >> 2) * (N * 128) + (kk & 3) * 32), kIdS, kk > 0);
           umma_commit(bar(GB_S + (g & 1)));
           umma_commit(bar(GB_KE + s));
-          if (j + 1 == it.n) umma_commit(bar(GB_QE + qb));
+          if (!C::Q_WITH_K && j + 1 == it.n) umma_commit(bar(GB_QE + qb));
         }
         __syncwarp();
         if (++s == ST) {
