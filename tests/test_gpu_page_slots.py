@@ -187,3 +187,27 @@ def test_binding_refusals():
                   ((i, i, t, i, span, 16), dict(rows=3, slots=torch.zeros(6, dtype=torch.int32, device="cuda")[::2]))):
         with pytest.raises(ValueError):
             sdpa_page_slots(*a, **kw)
+
+
+def test_outputs_made_in_one_allocation_are_apart():
+    """Each new output is contiguous, on its own bytes, and outlives the others."""
+    lens = torch.tensor([5, 0, 40], dtype=torch.int32, device="cuda")
+    new = torch.tensor([3, 2, 1], dtype=torch.int32, device="cuda")
+    table = torch.arange(12, dtype=torch.int32, device="cuda").view(3, 4)
+    ring = torch.arange(100, 150, dtype=torch.int32, device="cuda") % 50
+    span = torch.tensor([0, 20], device="cuda")
+    out = sdpa_page_slots(lens, new, table, ring, span, 16, rows=7)
+    assert [tuple(t.shape) for t in out] == [(7,), (7,), (4,), (3,), (2,)]
+    assert [t.dtype for t in out] == [torch.int32] * 4 + [torch.int64] and all(t.is_contiguous() for t in out)
+    ends = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in out)
+    assert all(a[1] <= b[0] for a, b in zip(ends, ends[1:]))
+    want = [t.clone() for t in out]
+    kept = out[2]
+    for t in out[:2]:
+        t.fill_(-7)
+    assert all(torch.equal(t, w) for t, w in zip(out[2:], want[2:]))
+    del out, t
+    torch.empty(4096, device="cuda").fill_(3)
+    assert torch.equal(kept, want[2])
+    empty = sdpa_page_slots(lens, new, table, ring, span, 16, rows=0)
+    assert empty[0].shape == (0,) and empty[3].tolist() == [5, 0, 40]
