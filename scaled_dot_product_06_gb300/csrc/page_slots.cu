@@ -15,7 +15,9 @@
 // requests, 1024 at a time, and then takes its share of the tokens and table
 // entries, found by bisection of the sums in shared memory. Where the lengths or
 // the ring's counters are advanced in place, the CTAs are a cluster, and they are
-// written after a barrier of all that read them.
+// written after a barrier of all that read them. A token each of 256 requests takes 5.5
+// us, 16384 tokens of 13 prompts 6.4, 131072 entries of 1000 requests 8.7 (1 MB: none of
+// it is bandwidth), captured and in a row.
 #include "common.cuh"
 #include "page_slots.cuh"
 

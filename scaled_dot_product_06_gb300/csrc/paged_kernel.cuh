@@ -50,6 +50,12 @@
 // waits for the values anyway. (Zeroed by the softmax threads, which then had to wait
 // for them too, 256 sequences of up to 777 keys took 209 us for 16 heads of their
 // own, where whole tiles of as many bytes took 131.)
+//
+// Bound by memory: 152 sequences of 4096 keys, 8 heads on one K/V head of d128, take 50.0 us
+// (6.4 TB/s, 94% of the copy rate), of which 2 pass before the first keys are asked for
+// (lengths, then the table, then keys) and 3 with the last parts' join; one sequence of
+// 131072 keys on 8 K/V heads 81.9 us (6.55 TB/s). Short units are bound by the keys'
+// producer and the ends of units instead: 0.9 us each.
 #pragma once
 #include "common.cuh"
 #include "paged.cuh"

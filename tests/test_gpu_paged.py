@@ -307,6 +307,17 @@ def test_two_streams_at_once():
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("long", [448, 1200], ids=["whole", "cut"])
+@pytest.mark.parametrize("h,d,d_v,t", [(3, 64, 64, "bf16"), (12, 128, 128, "fp16"), (48, 128, 128, "bf16"),
+                                       (6, 192, 128, "bf16"), (36, 192, 128, "fp16")])
+def test_short_units_one_behind_another(h, d, d_v, t, long):
+    """More units a CTA than buffers of queries, of none to a few tiles in all orders."""
+    lens = [(0, 1, 130, 257, 16, 128, 129, 384)[(i * i + 3 * i) % 8] for i in range(160)]
+    lens[77] = long
+    x = make(160, h, 3, 1, lens, 32, d, d_v, DTYPES[t], seed=d + h)
+    check(x, call(x), 1 / math.sqrt(d))
+
+
 def test_captured_calls_that_allocate():
     """Captured calls without a given workspace: each one's is handed on within the graph."""
     lens = [700, 3000, 1, 640, 2048, 999]
