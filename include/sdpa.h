@@ -611,7 +611,7 @@ sdpa_status_t sdpa_fwd_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, i
  *   Heads    h_kv divides h; query head i reads K/V head i / (h / h_kv).
  *   Workspace  sdpa_fwd_paged_workspace_size(...) bytes, 256-byte aligned, whose
  *            contents do not matter (none where a row of the table holds up to 512
- *            keys). Two calls that may run at the same time need one each. After a
+ *            keys; other calls may leave it alone, under a short window say). Two calls that may run at the same time need one each. After a
  *            device error a captured call's workspace is written anew (with
  *            anything) before the next replay.
  * The work is cut by the lengths, on the device: neither table_width nor a mix

@@ -11,15 +11,26 @@ constexpr int kPagedTile = 128;   // keys a tile
 constexpr int kPagedBox = 64;     // most keys of one copy
 constexpr int kPagedCost = 1;     // what a unit costs besides its key tiles, in tiles
 constexpr int kPagedGrid = 152;   // CTAs at most: one an SM
-constexpr int kPagedWhole = 4;    // key tiles up to which units are not cut
+// Key tiles up to which units are not cut, few units and many (a quarter of the CTAs). 80
+// units of 8 tiles (10 sequences of 1000 keys, 8 K/V heads) took 14.1 us cut and take 11.2, 512
+// ragged ones of up to 8 28.6 and 27.0, 4096 133.5 and 132.0; 8 units 8.2 cut and 9.1 whole.
+// (Up to 16 tiles: 64 units 13.2 cut and 15.5 whole, 512 46.9 and 47.4.) Up to 4: three units
+// 8.0 and 5.9, 600 units 28.4 and 25.1.
+constexpr int kPagedWhole = 4, kPagedWholeMany = 8;
 constexpr int kPagedGroup = 32;   // parts that are joined at once
 
 // A unit of work is a sequence, a K/V head and a block of its query rows. The
 // units of all sequences, each as long as its key tiles and kPagedCost, are one
 // line that is cut into as many equal runs as there are CTAs. Where a sequence can have
-// no more than kPagedWhole key tiles (the host knows what a row of the table holds, not
-// the lengths), a unit has a length of 1 and is not cut: then there is nothing to
-// join and no workspace.
+// no more than kPagedWhole... key tiles (the host knows what a row of the table holds and the
+// window, not the lengths), units are not cut: each is all of the run's in which it
+// begins; then there is nothing to join and no workspace. Where there are no more of them
+// than CTAs, or a sequence has one tile, each has a length of 1, so that no length is waited
+// for (2048 units of up to 100 keys 19.6 us for 20.2); else they have the lengths they
+// have cut (2048 of up to 512 keys 46.7 us, for 55.7 with a length of 1 each; 256 equal
+// ones of 512 keys 14.5 for 14.0).
+enum : int { kUnitsCut = 0, kUnitsAlike, kUnitsWhole };
+
 struct PagedParams {
   int B, H_kv;
   int R, s_q;              // query rows of a K/V head: (h / h_kv) * s_q, row x of token x % s_q
@@ -37,7 +48,7 @@ struct PagedParams {
   int capped;
   uint32_t q_box;          // bytes of a 64-column box of Q
   int grid;
-  int whole;               // units are not cut
+  int whole;               // kUnits...
   // Partial rows of units cut by a run's end: run c leaves slot 2 c + 1 for the unit whose
   // first part it has, and slot 2 c for the unit it begins within.
   float* part;             // [2 grid][rows a block][d_v]

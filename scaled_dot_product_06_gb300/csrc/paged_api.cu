@@ -98,8 +98,12 @@ unsigned long long next_nonce() {
   return (next.fetch_add(1, std::memory_order_relaxed) & ((1ull << 48) - 1)) | (1ull << 47);
 }
 
-// Whether the units of sequences of up to `capacity` keys are left whole.
-bool whole_units(int64_t capacity) { return capacity <= kPagedWhole * kPagedTile; }
+// Whether units of sequences of up to `capacity` keys are left whole, of which s_q
+// tokens see no more than left + s_q (left < 0: all), in up to a tile more.
+bool whole_units(int64_t capacity, int64_t units = 0, int64_t left = -1, int64_t s_q = 0) {
+  const int64_t most = (units >= kPagedGrid / 4 ? kPagedWholeMany : kPagedWhole) * kPagedTile;
+  return capacity <= most || (left >= 0 && left <= most && left + s_q + kPagedTile - 1 <= most);
+}
 
 // Heads and rows that both the size and the call check; *R: rows of a K/V head.
 sdpa_status_t check_rows_of(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, int64_t d_qk, int64_t d_v, int64_t* R) {
@@ -207,8 +211,9 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
   const int64_t capacity = n_pages > 0 ? table_width * page_size : 0;
   const int rows = paged_rows(static_cast<int>(R));
   const int64_t blocks = (R + rows - 1) / rows;
-  const bool whole = whole_units(table_width * page_size);
-  const int64_t line = b * h_kv * blocks * (whole ? 1 : (capacity + kPagedTile - 1) / kPagedTile + kPagedCost);
+  const int64_t units = b * h_kv * blocks;
+  const bool whole = whole_units(table_width * page_size, units, window_left, s_q);
+  const int64_t line = units * (whole ? kPagedWholeMany + kPagedCost : (capacity + kPagedTile - 1) / kPagedTile + kPagedCost);
   if (blocks * h_kv > kMaxInt / b || line > kMaxInt) return fail(SDPA_ERR_UNSUPPORTED, "too many key tiles");
   if (!q || !o || !lse || !seqlen_k || (capacity > 0 && !block_table)) return fail(SDPA_ERR_INVALID_ARG, "null pointer");
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(seqlen_k, 4) || !aligned(block_table, 4))
@@ -250,13 +255,13 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
   }
   const int box_q = static_cast<int>(std::min<int64_t>(R, rows));
   p.q_box = static_cast<uint32_t>(128 * box_q);
-  p.grid = static_cast<int>(std::min<int64_t>(kPagedGrid, line));
-  p.whole = whole ? 1 : 0;
+  p.grid = static_cast<int>(std::min<int64_t>(kPagedGrid, whole ? units : line));
+  p.whole = !whole ? kUnitsCut : units <= kPagedGrid || capacity <= kPagedTile ? kUnitsAlike : kUnitsWhole;
   if (!whole) {
     p.part = static_cast<float*>(workspace);
     p.part_lse = p.part + static_cast<int64_t>(2 * kPagedGrid) * rows * d_v;
     void* rest = p.part_lse + static_cast<int64_t>(2 * kPagedGrid) * rows;
-    if (2 * b * h_kv * blocks < p.grid) {  // more than two parts a unit (paged_kernel.cuh)
+    if (2 * units < p.grid) {  // more than two parts a unit (paged_kernel.cuh)
       p.runs = static_cast<int4*>(rest);
     } else {
       p.words = static_cast<unsigned long long*>(rest);

@@ -31,7 +31,8 @@
 // are): a kernel of its own for that (paged_join.cu) takes 6 us from the end of one to
 // the next call's first look at memory: 96 sequences of up to 5000 keys on one K/V
 // head 31.7 us for 33.6. Where there are more, that kernel does, with all SMs: one
-// sequence of 131072 keys, 8 K/V heads, 19 parts each, 81.3 us for 84.2.
+// sequence of 131072 keys, 8 K/V heads, 19 parts each, 81.3 us for 84.2. Units of few
+// tiles are not cut (paged.cuh).
 //
 // One persistent CTA an SM. Roles: two warpgroups of softmax threads (at NR = 8 and 16 they
 // take the key tiles in turns, each with a maximum, sum and O of its own, joined at
@@ -296,7 +297,7 @@ __device__ __noinline__ bool paged_join(float* part, float* part_lse, unsigned l
 
 // How long a unit of the sequence is on the line.
 __device__ __forceinline__ int paged_weight(const PagedParams& p, const PagedSpan& s) {
-  return p.whole ? 1 : s.n + kPagedCost;
+  return p.whole == kUnitsAlike ? 1 : s.n + kPagedCost;
 }
 
 template <int DQK, int DV, bool BF16, int NR>
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
   uint32_t sum = 0;
 #pragma unroll 1
   for (int i = tid * per; i < min(p.B, (tid + 1) * per); ++i)
-    sum += p.whole ? 1u : static_cast<uint32_t>(paged_weight(p, paged_span(p, p.seqlen[i])));
+    sum += p.whole == kUnitsAlike ? 1u : static_cast<uint32_t>(paged_weight(p, paged_span(p, p.seqlen[i])));
   sum *= static_cast<uint32_t>(units);
   uint32_t upto = sum;
 #pragma unroll
@@ -482,7 +483,9 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     while (left > 0) {
       const int w = paged_weight(p, sp);
       const int take = static_cast<int>(min(left, static_cast<uint32_t>(w - pos)));
-      const int t0 = p.whole ? 0 : max(pos - kPagedCost, 0), t1 = p.whole ? sp.n : max(pos + take - kPagedCost, 0);
+      // (a unit that is not cut is all of the run's in which it begins)
+      const int t0 = p.whole ? (pos > 0 ? sp.n : 0) : max(pos - kPagedCost, 0);
+      const int t1 = p.whole ? sp.n : max(pos + take - kPagedCost, 0);
       const bool none = sp.n == 0 && pos == 0;
       if (t1 > t0 || none) {
         PagedItem it;

@@ -244,12 +244,13 @@ def test_pools_past_32_bits():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-@pytest.mark.parametrize("batches", [(3, 1), (80, 50)], ids=["many parts", "few parts"])
-def test_captured_graphs_that_share_a_workspace(batches):
+@pytest.mark.parametrize("batches,more", [((3, 1), 0), ((80, 50), 0), ((80, 50), 700)],
+                         ids=["many parts", "whole", "few parts"])
+def test_captured_graphs_that_share_a_workspace(batches, more):
     """Two captured calls with one workspace, replayed in turn on lengths that change,
     and that a copy within the graph brings."""
     page, h_kv = 16, 2
-    lens = [6000 // b + 600 for b in batches]
+    lens = [6000 // b + 600 + more for b in batches]
     xs = [make(b, 16, h_kv, 1, [n] * b, page, 128, 128, torch.bfloat16, seed=b, garbage=False)
           for b, n in zip(batches, lens)]
     ws = torch.full((max(sdpa_fwd_paged_workspace_size(16, h_kv, 1, 128, 128, page, x["block_table"].shape[1])
@@ -316,6 +317,25 @@ def test_short_units_one_behind_another(h, d, d_v, t, long):
     lens[77] = long
     x = make(160, h, 3, 1, lens, 32, d, d_v, DTYPES[t], seed=d + h)
     check(x, call(x), 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("left,count", [(40, 8), (383, 8), (384, 8), (385, 8), (383, 128), (894, 128), (895, 128),
+                                        (896, 128)], ids=lambda n: str(n))
+def test_windows_of_a_few_tiles(left, count):
+    """Windows around the four and eight tiles up to which few and many units stay whole, at
+    all places of a tile."""
+    lens = [1300 + i * 128 // count + i for i in range(count)] + [0, 1, 384, 385, 386]
+    x = make(len(lens), 4, 2, 2, lens, 32, 64, 64, torch.bfloat16, seed=left)
+    check(x, call(x, window_left=left), 1 / 8, left=left)
+
+
+@pytest.mark.parametrize("count", [1, 18, 19, 75, 76, 77, 200])
+@pytest.mark.parametrize("longest", [480, 992, 1000])
+def test_units_cut_or_whole(count, longest):
+    """Ragged sequences on both sides of the sizes and counts at which units are cut."""
+    lens = [(longest * (7 * i + 3)) // 11 % longest for i in range(count - 1)] + [longest]
+    x = make(count, 2, 2, 1, lens, 16, 64, 64, torch.float16, seed=count)
+    check(x, call(x), 1 / 8)
 
 
 def test_captured_calls_that_allocate():
