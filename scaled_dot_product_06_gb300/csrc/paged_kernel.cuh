@@ -37,7 +37,8 @@
 // One persistent CTA an SM. Roles: two warpgroups of softmax threads (at NR = 8 and 16 they
 // take the key tiles in turns, each with a maximum, sum and O of its own, joined at
 // the unit's end by the one that had the last tile, while the other goes on; at 32
-// and 64 each has half of the rows), two producer warps, which both walk the run and
+// and 64 each has half of the rows: in turns, 32 columns a thread spill, and 64 sequences
+// of 4096 keys on 4 K/V heads of d64 took 75.7 us for 54.2), two producer warps, which both walk the run and
 // copy pages by TMA, one the keys, the other the values (a copy of a small page
 // takes its warp longer to issue than memory to deliver), and two MMA issuers, one for
 // S^T, up to two tiles ahead, one for O^T: the products are so small that a tile's
