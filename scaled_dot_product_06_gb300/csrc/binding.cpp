@@ -76,7 +76,12 @@ template <typename T = void>
 T* flat(const char* name, const Tensor& t, ScalarType type, const Place& at, IntArrayRef shape) {
   if (t.scalar_type() != type || !t.is_cuda() || t.get_device() != at.index || !t.is_contiguous())
     refuse("%s must be a contiguous torch.%s tensor on the device of %s", name,
-           type == at::kInt ? "int32" : type == at::kLong ? "int64" : type == at::kFloat ? "float32" : type == at::kHalf ? "float16" : "bfloat16", at.of);
+           type == at::kInt     ? "int32"
+           : type == at::kLong  ? "int64"
+           : type == at::kFloat ? "float32"
+           : type == at::kHalf  ? "float16"
+                                : "bfloat16",
+           at.of);
   check_shape(name, t, shape);
   return static_cast<T*>(t.data_ptr());
 }

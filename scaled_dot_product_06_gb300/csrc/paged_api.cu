@@ -213,7 +213,8 @@ sdpa_status_t sdpa_fwd_paged(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, in
   const int64_t blocks = (R + rows - 1) / rows;
   const int64_t units = b * h_kv * blocks;
   const bool whole = whole_units(table_width * page_size, units, window_left, s_q);
-  const int64_t line = units * (whole ? kPagedWholeMany + kPagedCost : (capacity + kPagedTile - 1) / kPagedTile + kPagedCost);
+  const int64_t line =
+      units * ((whole ? kPagedWholeMany : (capacity + kPagedTile - 1) / kPagedTile) + kPagedCost);
   if (blocks * h_kv > kMaxInt / b || line > kMaxInt) return fail(SDPA_ERR_UNSUPPORTED, "too many key tiles");
   if (!q || !o || !lse || !seqlen_k || (capacity > 0 && !block_table)) return fail(SDPA_ERR_INVALID_ARG, "null pointer");
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(seqlen_k, 4) || !aligned(block_table, 4))

@@ -38,12 +38,12 @@
 // take the key tiles in turns, each with a maximum, sum and O of its own, joined at
 // the unit's end by the one that had the last tile, while the other goes on; at 32
 // and 64 each has half of the rows: in turns, 32 columns a thread spill, and 64 sequences
-// of 4096 keys on 4 K/V heads of d64 took 75.7 us for 54.2), two producer warps, which both walk the run and
-// copy pages by TMA, one the keys, the other the values (a copy of a small page
-// takes its warp longer to issue than memory to deliver), and two MMA issuers, one for
-// S^T, up to two tiles ahead, one for O^T: the products are so small that a tile's
-// instructions and waits, not the tensor cores, bound an issuer (1900 cycles a tile
-// of d = 64 for one warp with both). The keys' producer also copies the queries and
+// of 4096 keys on 4 K/V heads of d64 took 75.7 us for 54.2), two producer warps, which
+// both walk the run and copy pages by TMA, one the keys, the other the values (a copy of
+// a small page takes its warp longer to issue than memory to deliver), and two MMA
+// issuers, one for S^T, up to two tiles ahead, one for O^T: the products are so small that
+// a tile's instructions and waits, not the tensor cores, bound an issuer (1900 cycles a
+// tile of d = 64 for one warp with both). The keys' producer also copies the queries and
 // tells the others the units through a ring.
 // Rows of a tile that no query sees (behind the last key, before the window,
 // in pages that are not read) may hold anything. Their scores are masked; their
@@ -111,7 +111,8 @@ struct PagedCfg {
 // unit full and read, statistics handed over, ring of units.
 enum : int { GB_KF = 0, GB_KE = GB_KF + 6, GB_VF = GB_KE + 6, GB_VE = GB_VF + 6, GB_Q = GB_VE + 6, GB_QE = GB_Q + 2,
              GB_S = GB_QE + 2, GB_P = GB_S + 2, GB_PV = GB_P + 2, GB_O = GB_PV + 2, GB_OE = GB_O + 2,
-             GB_ST = GB_OE + 2, GB_I = GB_ST + 4, GB_IE = GB_I + 4, GB_DRAIN = GB_IE + 4, GB_START = GB_DRAIN + 2, GB_COUNT = GB_START + 2 };
+             GB_ST = GB_OE + 2, GB_I = GB_ST + 4, GB_IE = GB_I + 4, GB_DRAIN = GB_IE + 4, GB_START = GB_DRAIN + 2,
+             GB_COUNT = GB_START + 2 };
 
 // One unit's part of a run, as the producer tells it.
 struct PagedItem {
@@ -477,7 +478,8 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
       lens_ahead = length(l0 + 32 + lane);
     }
     auto span_of = [&](int i) {  // i in [l0, l0 + 64)
-      const int near = __shfl_sync(0xffffffffu, lens, (i - l0) & 31), far = __shfl_sync(0xffffffffu, lens_ahead, (i - l0) & 31);
+      const int near = __shfl_sync(0xffffffffu, lens, (i - l0) & 31);
+      const int far = __shfl_sync(0xffffffffu, lens_ahead, (i - l0) & 31);
       return paged_span(p, i - l0 < 32 ? near : far);
     };
     bool ahead_known = false;  // sp_next is that of sequence i + 1
@@ -546,7 +548,8 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
             if (elect_one_sync()) {
               const uint32_t b = bar(full + s), rows = static_cast<uint32_t>(p.box) * 128u;  // bytes of a box
               const bool with_q = C::Q_WITH_K && keys && j == 0;
-              mbar_arrive_expect_tx(b, static_cast<uint32_t>(hi - lo) * rows * width + (with_q ? (DQK / 64) * p.q_box : 0u));
+              mbar_arrive_expect_tx(b, static_cast<uint32_t>(hi - lo) * rows * width +
+                                           (with_q ? (DQK / 64) * p.q_box : 0u));
               if (with_q) copy_q(b);
               uint32_t dst = ring + s * stage_bytes + static_cast<uint32_t>(lo - box0) * rows;
 #pragma unroll 1
@@ -611,7 +614,8 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     if (*abort_flag) {
 #pragma unroll 1
       for (int b = 0; b < C::Q_BUFS; ++b)
-        if (!C::Q_WITH_K && keys && nq > b) mbar_wait(bar(GB_Q + b), ((nq - 1 - b) / C::Q_BUFS) & 1, ec, kSiteDrain, false);
+        if (!C::Q_WITH_K && keys && nq > b)
+          mbar_wait(bar(GB_Q + b), ((nq - 1 - b) / C::Q_BUFS) & 1, ec, kSiteDrain, false);
 #pragma unroll 1
       for (int s = 0; s < ST; ++s)
         if (nt > s) mbar_wait(bar(full + s), ((nt - 1 - s) / ST) & 1, ec, kSiteDrain, false);
