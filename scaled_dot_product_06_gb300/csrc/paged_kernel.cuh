@@ -18,7 +18,9 @@
 // warp busy with 128 columns while the others idle.) The products read their long
 // operand from shared memory, and a few columns more cost them nothing: P goes in
 // as a high and a low part, each rounded to 16 bits, side by side, whose two O are
-// added at the end, so that its rounding (2^-9 in bf16, as much as O's own) is gone.
+// added at the end, so that its rounding (2^-8 in bf16, as much as O's own) is gone. In
+// fp16 the low part is held 2^18 times as large: what is below 2^-25, which the high part
+// loses (131072 keys of 2^-25.4 beside one of 1 are 2^-8.4 of O), is in it down to 2^-43.
 //
 // The lengths are known on the device only. All units (sequence, K/V head, row
 // block) in a row, each as long as its key tiles, are one line, cut into equal
@@ -810,6 +812,9 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
     // without asking for their maximum, which takes the warpgroup longer than the
     // softmax of the tile.
     constexpr float kFar = BF16 ? 60.f : 8.f;
+    // Factor of P's low part. fp16: P is at most 2^kFar, what its high part leaves 2^-12 of
+    // that, so the low part at most 2^14; bf16 has fp32's exponents and needs none.
+    constexpr float kLow = BF16 ? 1.f : 0x1p18f;
     constexpr float kNone = 1e30f;  // -m of a row without a score: any score then grows it
     int u = 0, g0 = 0, q = 0, pairs = 0;  // item, its first tile, items with keys, items of both warpgroups
     bool ok = true, left_all = false;
@@ -943,7 +948,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
           for (int i = 0; i < 4; ++i) {
             hi[i] = pack2<BF16>(x[e + 2 * i], x[e + 2 * i + 1]);
             const float2 f = unpack2<BF16>(hi[i]);
-            lo[i] = pack2<BF16>(x[e + 2 * i] - f.x, x[e + 2 * i + 1] - f.y);
+            lo[i] = pack2<BF16>((x[e + 2 * i] - f.x) * kLow, (x[e + 2 * i + 1] - f.y) * kLow);
           }
           *reinterpret_cast<uint4*>(to + chunk_at((col0 + e) / 8)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(to + chunk_at((NR + col0 + e) / 8)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -1009,7 +1014,7 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < NC; ++e) {
-              const float v = f[e] == 0.f ? 0.f : (hi[e] + lo[e]) * f[e];
+              const float v = f[e] == 0.f ? 0.f : fmaf(lo[e], 1.f / kLow, hi[e]) * f[e];
               o[e] = add ? o[e] + v : v;
             }
           };
