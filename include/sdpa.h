@@ -605,7 +605,11 @@ sdpa_status_t sdpa_fwd_prefix(int64_t b, int64_t h, int64_t h_kv, int64_t s_q, i
  *            n_pages) reads as rows of zeros.
  *            Rows of the pages that no new token sees may hold anything, NaN too.
  *            Values that only some of the new tokens see must be finite: they
- *            enter the others' sums with a weight of 0. Keys and queries may be
+ *            enter the others' sums with a weight of 0. One that all of them see
+ *            may be infinite or NaN: so are the elements of O that it is summed in
+ *            (an infinite one gives NaN beside the other infinity, and where its key
+ *            weighs less than 2^-24, in bf16 2^-60, of the row's largest). Finite ones
+ *            in bf16 stay below 2^67 divided by the keys. Keys and queries may be
  *            NaN: the rows that see one get NaN in O and LSE, no other row does.
  *   scale    as in sdpa_fwd; softcap 0 (none) or as in the capped calls.
  *   Heads    h_kv divides h; query head i reads K/V head i / (h / h_kv).

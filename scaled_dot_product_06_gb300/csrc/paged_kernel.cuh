@@ -1014,7 +1014,9 @@ __global__ void __launch_bounds__(PagedCfg<DQK, DV, NR>::THREADS, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < NC; ++e) {
-              const float v = f[e] == 0.f ? 0.f : fmaf(lo[e], 1.f / kLow, hi[e]) * f[e];
+              // (an infinite value times a low part of 0 or below would make it NaN)
+              const float sum = fabsf(hi[e]) < -SDPA_NEG_INF ? fmaf(lo[e], 1.f / kLow, hi[e]) : hi[e];
+              const float v = f[e] == 0.f ? 0.f : sum * f[e];
               o[e] = add ? o[e] + v : v;
             }
           };
