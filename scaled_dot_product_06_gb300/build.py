@@ -5,7 +5,8 @@ Each CUDA translation unit under ``csrc/`` is compiled in parallel into
 is linked statically; the driver entry point for TMA descriptor encoding is
 looked up at run time, so the library loads on machines without a GPU.
 ``_binding.so``, the native binding of the calls with the shortest kernels, is
-compiled by g++ against torch's headers and linked to that library.
+compiled by g++ against torch's headers and linked to that library. Where torch is
+not installed it is left out: the library and its C entry points do not need it.
 """
 from __future__ import annotations
 
@@ -58,8 +59,16 @@ def _run(cmd: list[str], what: str) -> None:
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
-def _compile_binding() -> str:
-    import torch
+def _torch():
+    """The installed torch, or None."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch
+
+
+def _compile_binding(torch) -> str:
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     obj = os.path.join(BUILD, "binding.o")
@@ -70,8 +79,7 @@ def _compile_binding() -> str:
     return obj
 
 
-def _link_binding(obj: str) -> None:
-    import torch
+def _link_binding(torch, obj: str) -> None:
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L" + HERE, "-l:libsdpa.so",
           "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda",
@@ -83,15 +91,21 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     """Compile every translation unit and link libsdpa.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(len(SOURCES) + 1, os.cpu_count() or 1)
+    torch = _torch()
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = None if torch is None else ex.submit(_compile_binding, torch)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs]
     _run(cmd, "link of libsdpa.so")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    # the library is there whatever becomes of the binding, and no binding of another build beside it
+    if os.path.exists(BINDING):
+        os.remove(BINDING)
+    if binding is None:
+        sys.stderr.write("torch is not installed: libsdpa.so is built, _binding.so is left out\n")
+    else:
+        _link_binding(torch, binding.result())
     return LIB
 
 
