@@ -162,11 +162,19 @@ def binding():
         import importlib.machinery
         import importlib.util
 
-        import torch  # noqa: F401  (the libraries that it is linked to)
+        import torch  # (the libraries that it is linked to)
+        again = f"build it again beside torch {torch.__version__}"
         spec = importlib.util.spec_from_file_location(
             "_binding", path, loader=importlib.machinery.ExtensionFileLoader("_binding", path))
-        _binding = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_binding)
+        try:
+            module = importlib.util.module_from_spec(spec)
+        except ImportError as e:
+            raise RuntimeError(f"{path} does not load: {again} ({e})") from e
+        built = getattr(module, "torch_version", "another version")
+        if built != str(torch.__version__):
+            raise RuntimeError(f"{path} was compiled against torch {built}: {again}")
+        spec.loader.exec_module(module)
+        _binding = module
     return _binding
 
 

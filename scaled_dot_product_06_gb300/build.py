@@ -73,6 +73,7 @@ def _compile_binding(torch) -> str:
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     obj = os.path.join(BUILD, "binding.o")
     _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          f'-DSDPA_TORCH_VERSION="{torch.__version__}"',
           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c", os.path.join(CSRC, "binding.cpp"),
           "-o", obj], "g++ on binding.cpp")

@@ -397,4 +397,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// torch_version: the torch that this was compiled against, which the Python side compares
+// with the one that it finds.
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", SDPA_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}
