@@ -47,7 +47,6 @@ struct NormRopeParams {
   Divider n_tb;    // blocks of tokens (norm_rope_plan)
   int d, rot, interleaved;
   int seg;         // heads a work unit walks (norm_rope_plan)
-  int paired;      // the walk of a token's keys goes on with its values (forward)
   float eps;
   int weight_fp32;       // weights are fp32 (else the io type)
   const float* cos;      // [n_pos][rot / 2]
