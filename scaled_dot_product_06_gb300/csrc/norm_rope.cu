@@ -203,9 +203,10 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_fwd_kernel(const __grid
   __shared__ uint4 ring[kRing][kThreads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / C::L, l = lane - sub * C::L;  // row of the warp, lane of the row
-  // Launched while the kernel before runs out (256 decoding tokens of 32 + 2 x 8 heads 3.9
-  // us for 4.4): memory is looked at from here on, by loads that are not the read-only
-  // ones, which the compiler may put ahead of this. The kernel behind is not
+  // Launched while the kernel before runs out (256 decoding tokens of 32 + 2 x 4 heads 3.9
+  // us for 4.4; directly behind the attention over pages, where a model has the
+  // projections, a layer of both takes 0.3 us longer): memory is looked at from here on, by
+  // loads that are not the read-only ones, which the compiler may put ahead of this. The kernel behind is not
   // called up early: its blocks beside this one's took 9.4 us for 8.0 of 3 x 777 tokens d192.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const RowKind& k = p.kind[kind_of_block(p, blockIdx.x)];

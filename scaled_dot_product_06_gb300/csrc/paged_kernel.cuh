@@ -24,7 +24,7 @@
 //
 // The lengths are known on the device only. All units (sequence, K/V head, row
 // block) in a row, each as long as its key tiles, are one line, cut into equal
-// runs, one for each CTA: any mix of lengths ends at the same time on all SMs. A
+// runs, one for each CTA: any mix of lengths ends at about the same time on all SMs. A
 // unit that a run's end cuts leaves normalised fp32 rows O_s and their log2-sum-exps
 // L_s, at most two slots a CTA, which are joined,
 //   L = log2 sum_s 2^L_s,  O = sum_s 2^(L_s - L) O_s,
@@ -133,10 +133,11 @@ __device__ __forceinline__ uint64_t paged_desc_p(uint32_t saddr, int pitch) {
   return d;
 }
 
-// tanh to about 2^-23 relative: z + z^3 q(z^2) up to 5/8, q a polynomial fitted to
-// it by reweighted least squares (2^-27.7), else 1 - 2 / (1 + e^(2 |z|)), which
-// loses nothing there. (cap_r8's form is good to 2^-20 of the cap, which a sum of
-// many rows, LSE, shows; here the keys' stream leaves time for this one.)
+// tanh to 2^-22.2 relative (against 64 bits, all fp32 numbers from 2^-20 to 12): z + z^3
+// q(z^2) up to 5/8, q a polynomial fitted to it by reweighted least squares (itself good to
+// 2^-26.8; 2^-23.6 with its roundings), else 1 - 2 / (1 + e^(2 |z|)), which is at its worst
+// just behind 5/8, 2^-22.3, and from 1 on good to 2^-23.1. (cap_r8's form is good to 2^-20
+// of the cap, which a sum of many rows, LSE, shows; here the keys' stream leaves time for this one.)
 __device__ __forceinline__ float paged_tanh(float z) {
   const float a = fabsf(z), z2 = z * z;
   const float far = copysignf(fmaf(-2.f, rcp(1.f + ex2(a * (2.f * kLog2e))), 1.f), z);

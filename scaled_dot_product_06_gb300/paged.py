@@ -26,7 +26,8 @@ def sdpa_page_slots(seqlens, new_tokens, block_table, free_pages, free_range, pa
     [b + 1] that the packed calls take (else None); the new lengths, for
     sdpa_fwd_paged; the new ring. seqlens and free_range may be given as
     seqlens_out and free_range_out. A request for which there is no room (pages, width
-    of the table, entries) gets slots of -1 and keeps its length."""
+    of the table, entries) gets slots of -1 and keeps its length. The outputs that are
+    not given share one allocation: while one of them is kept, all are."""
     return call_native("page_slots", stream, seqlens, (slots, positions, starts, seqlens_out, free_range_out), seqlens,
                        new_tokens, block_table, free_pages, free_range, page_size, rows, width, slots, positions,
                        starts, seqlens_out, free_range_out)
@@ -54,6 +55,8 @@ def sdpa_fwd_paged(q, k_pages, v_pages, block_table, seqlens_k, *, scale=None, s
     the s_q new tokens' among them (appended beforehand). New token t sees keys up to
     its own place seqlens_k - s_q + t, the last window_left + 1 of them if that is
     given. What the pages hold besides is not looked at. softcap as in sdpa_fwd.
-    The workspace (sdpa_fwd_paged_workspace_size bytes) is allocated when not given."""
+    The workspace (sdpa_fwd_paged_workspace_size bytes) is allocated when not given.
+    Short sequences are 0.5 to 3 us faster under a table whose rows hold no more than
+    512 keys."""
     return call_native("fwd_paged", stream, q, (out, lse), q, k_pages, v_pages, block_table, seqlens_k, scale, softcap,
                        window_left, out, lse, workspace)
