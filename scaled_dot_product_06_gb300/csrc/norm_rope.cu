@@ -206,8 +206,9 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_fwd_kernel(const __grid
   // Launched while the kernel before runs out (256 decoding tokens of 32 + 2 x 4 heads 3.9
   // us for 4.4; directly behind the attention over pages, where a model has the
   // projections, a layer of both takes 0.3 us longer): memory is looked at from here on, by
-  // loads that are not the read-only ones, which the compiler may put ahead of this. The kernel behind is not
-  // called up early: its blocks beside this one's took 9.4 us for 8.0 of 3 x 777 tokens d192.
+  // loads that are not the read-only ones, which the compiler may put ahead of this. The
+  // kernel behind is not called up early: its blocks beside this one's took 9.4 us for 8.0
+  // of 3 x 777 tokens d192.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const RowKind& k = p.kind[kind_of_block(p, blockIdx.x)];
   const uint32_t u = (blockIdx.x - k.block0) * C::WARPS + warp;
